@@ -25,6 +25,12 @@ call raises.
     qgemm_quant_f8_block(X, out=None, scales=None)        -> (Q, S)
     qgemm_quant_mx(fmt, X, out=None, scales=None)         -> (Q, S)
 
+and the operators a decoder layer runs between its GEMMs (``layer.py``):
+
+    qgemm_rmsnorm_quant_i8_rowwise / _f8_pertoken / _f8_block
+        (X, gamma, eps=1e-6, residual=None, residual_out=None, out=None, scale=None)  -> (Q, scale, residual_out)
+    qgemm_rmsnorm_quant_mx(fmt, X, gamma, ...)            -> (Q, S, residual_out)
+
 Operands are [rows, K] with unit stride along K (row stride may exceed the
 row; it is passed as lda).  ``out`` may be a view of a wider buffer (row
 stride = ldc).  Errors in arguments raise ValueError; a device or HIP
@@ -57,6 +63,8 @@ EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f
            "qgemm_prepacked_b_bytes", "qgemm_prepack_b", "qgemm_i8_rowwise_prepacked",
            "qgemm_f8_pertoken_prepacked", "qgemm_f8_blockscale_prepacked", "qgemm_mx_prepacked",
            "qgemm_quant_f8_pertoken", "qgemm_quant_f8_block", "qgemm_quant_mx",
+           "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_f8_block",
+           "qgemm_rmsnorm_quant_mx",
            "qgemm_last_error", "qgemm_status_string", "qgemm_select_tile",
            "qgemm_tile_rows", "qgemm_force_tile")
 
@@ -122,6 +130,15 @@ def declare(L):
     L.qgemm_quant_f8_block.argtypes = [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]
     L.qgemm_quant_mx.restype = st
     L.qgemm_quant_mx.argtypes = [ctypes.c_int, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]
+    norm = [_P, _I64, _P, _I64, _P, ctypes.c_float, _P, _I64, _P, _I64, _P]
+    L.qgemm_rmsnorm_quant_i8_rowwise.restype = st
+    L.qgemm_rmsnorm_quant_i8_rowwise.argtypes = norm + [_I64, _I64, _P]
+    L.qgemm_rmsnorm_quant_f8_pertoken.restype = st
+    L.qgemm_rmsnorm_quant_f8_pertoken.argtypes = norm + [_I64, _I64, _P]
+    L.qgemm_rmsnorm_quant_f8_block.restype = st
+    L.qgemm_rmsnorm_quant_f8_block.argtypes = norm + [_I64, _I64, _I64, _P]
+    L.qgemm_rmsnorm_quant_mx.restype = st
+    L.qgemm_rmsnorm_quant_mx.argtypes = [ctypes.c_int] + norm + [_I64, _I64, _I64, _P]
     L.qgemm_last_error.restype = ctypes.c_char_p
     L.qgemm_last_error.argtypes = []
     L.qgemm_status_string.restype = ctypes.c_char_p
@@ -683,3 +700,7 @@ def qgemm_mx_prepacked(fmt, A, Bp, scale_a, scale_b, b_layout, bias=None, out=No
         _check(lib().qgemm_mx_prepacked(fmt, _ptr(A), lda, _ptr(Bp.data), _ptr(sa), _ptr(sb), b_layout,
                                         _ptr(bias), _ptr(out), _ldc(out, N), M, N, K, _stream(A.device, stream)))
     return out
+
+
+from .layer import (qgemm_rmsnorm_quant_f8_block, qgemm_rmsnorm_quant_f8_pertoken,  # noqa: E402,F401
+                    qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx)

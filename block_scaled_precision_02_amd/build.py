@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqgemm.so")
 SOURCES = ["qgemm_api.cpp", "qgemm_i8.hip", "qgemm_f8.hip", "qgemm_mx8.hip", "qgemm_mx4.hip", "qgemm_f8b.hip", "qgemm_mx84.hip", "qgemm_mx48.hip", "qgemm_mx4h.hip", "qgemm_mx6.hip",
-           "qgemm_quant.hip", "qgemm_pack.hip"]
+           "qgemm_quant.hip", "qgemm_pack.hip",
+           "layer/layer_api.cpp", "layer/norm.hip"]
 # Per-source extra flags.  The blockscale kernel folds its MFMA partial sums
 # into the totals with VALU FMAs every 128 K elements; keeping the MFMA
 # results in VGPRs (rather than the accumulator registers, which the VALU
@@ -38,7 +39,7 @@ LIB_SYNC = os.path.join(HERE, "libqgemm_sync.so")
 
 
 def _compile(src, twin=False):
-    obj = os.path.join(BUILD_SYNC if twin else BUILD, src + ".o")
+    obj = os.path.join(BUILD_SYNC if twin else BUILD, src.replace("/", "_") + ".o")
     cmd = ([HIPCC] + FLAGS + EXTRA_FLAGS.get(src, []) + (["-DQGEMM_SYNC_TWIN=1"] if twin else []) +
            ["-c", os.path.join(CSRC, src), "-o", obj])
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -83,7 +84,7 @@ _REMARKS = (("VGPRs", "VGPRs"), ("AGPRs", "AGPRs"), ("TotalSGPRs", "SGPRs"), ("S
 def _audit(src):
     import re
     cmd = ([HIPCC] + FLAGS + EXTRA_FLAGS.get(src, []) + ["-Rpass-analysis=kernel-resource-usage", "-c",
-           os.path.join(CSRC, src), "-o", os.path.join(BUILD, src + ".audit.o")])
+           os.path.join(CSRC, src), "-o", os.path.join(BUILD, src.replace("/", "_") + ".audit.o")])
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}")

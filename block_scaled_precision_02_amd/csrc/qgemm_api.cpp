@@ -19,6 +19,7 @@
 #include <string>
 
 #include "../../include/qgemm.h"
+#include "qgemm_host.hpp"
 #include "qgemm_launch.hpp"
 #include "qgemm_pack.hpp"
 #include "qgemm_quant.hpp"
@@ -26,11 +27,12 @@
 using namespace qgemm;
 
 namespace {
-
 thread_local std::string g_last_error;
 thread_local int g_forced_tile = -1;
+}  // namespace
 
-qgemm_status fail(qgemm_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace qgemm {
+
 qgemm_status fail(qgemm_status st, const char *fmt, ...)
 {
     char buf[512];
@@ -42,10 +44,11 @@ qgemm_status fail(qgemm_status st, const char *fmt, ...)
     return st;
 }
 
-constexpr int64_t I8_K_MAX = 131071;   // K * 128 * 128 < 2^31
-constexpr int64_t LD_LIMIT = (int64_t)1 << 31;
+}  // namespace qgemm
 
-bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
+namespace {
+
+constexpr int64_t I8_K_MAX = 131071;   // K * 128 * 128 < 2^31
 
 // ------------------------------------------------------------ device check
 // gfx950 or nothing.  The answer per device is cached after the first query.
@@ -57,6 +60,10 @@ bool is_gfx950(const char *name)
 {
     return strncmp(name, "gfx950", 6) == 0 && (name[6] == 0 || name[6] == ':');
 }
+
+}  // namespace
+
+namespace qgemm {
 
 // Test hook: QGEMM_INJECT_LAUNCH_ERROR=<hipError_t code> makes every call
 // that passed its checks report that launch error (QGEMM_ERR_HIP) instead of
@@ -97,6 +104,10 @@ qgemm_status check_device()
         return fail(QGEMM_ERR_HIP, "hipGetDeviceProperties failed for device %d", dev);
     return fail(QGEMM_ERR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
 }
+
+}  // namespace qgemm
+
+namespace {
 
 // ------------------------------------------------------------ tile table
 // A launch runs in rounds of (CUs x workgroups per CU) tiles; a round lasts
@@ -211,13 +222,6 @@ qgemm_status check_bias(const uint16_t *bias)
     return QGEMM_OK;
 }
 
-#define TRY(x)                                  \
-    do {                                        \
-        qgemm_status st_ = (x);                 \
-        if (st_ != QGEMM_OK)                    \
-            return st_;                         \
-    } while (0)
-
 Params base_params(const void *A, int64_t lda, const void *B, int64_t ldb, void *C, int64_t ldc, Shape s,
                    int64_t kbytes, int tile)
 {
@@ -257,23 +261,6 @@ qgemm_status check_grid(const Params &p)
     if ((int64_t)p.tiles_m * p.tiles_n >= LD_LIMIT)
         return fail(QGEMM_ERR_BAD_SHAPE, "grid of %d x %d tiles is too large", p.tiles_m, p.tiles_n);
     return QGEMM_OK;
-}
-
-qgemm_status finish(hipError_t e)
-{
-    if (e != hipSuccess)
-        return fail(QGEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
-    return QGEMM_OK;
-}
-
-// Every launch goes through here: the kernel launch (f), or the injected
-// launch error, which leaves the output and everything else untouched.
-template <class F>
-qgemm_status launch(F &&f)
-{
-    if (const int e = injected_launch_error())
-        return fail(QGEMM_ERR_HIP, "kernel launch: injected error %d", e);
-    return finish(f());
 }
 
 // The LDS-fetch kernels (tiles 4-7) run tiles whose K is a whole number of

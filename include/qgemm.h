@@ -324,6 +324,55 @@ qgemm_status qgemm_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t ldx, vo
 qgemm_status qgemm_quant_f8_block(const uint16_t *X, int64_t ldx, uint8_t *Q, int64_t ldq, float *S, int64_t lds,
                                   int64_t M, int64_t K, void *stream);
 
+/* ---------------------------------------------------------------------
+ * Decoder-layer operators: what runs between the GEMMs of a served layer.
+ * Conventions as above (caller-owned device buffers, asynchronous on stream,
+ * arguments checked on the host, nothing allocated).
+ * --------------------------------------------------------------------- */
+
+/* Root-mean-square norm of X + R with quantised output: the A operand and
+ * scale_a of the GEMM that follows, from the layer's activations and its
+ * residual stream in one pass.  Per row m, in binary32:
+ *   h    = X + R                       (X alone where R is NULL)
+ *   Rout = bf16(h)                     (not written where Rout is NULL)
+ *   y    = (h * gamma) * 1/sqrt(mean(h^2) + eps)
+ *   Q, scales = the quantiser's rule on y (y is not rounded to bf16 first):
+ *     i8_rowwise   scale[m] = amax|y| / 127, Q = int8 nearest even of y/scale
+ *     f8_pertoken  as qgemm_quant_f8_pertoken, one scale a row
+ *     f8_block     as qgemm_quant_f8_block, one scale per 128 elements
+ *     mx           as qgemm_quant_mx, one ue8m0 scale per 32 elements
+ * Quotients y/scale may differ by one unit in the last place of binary32
+ * from the divided ones.  A row (block) whose y is all zero gets scale 0 and
+ * zero codes.
+ *   X      [M, K] bf16, row stride ldx ELEMENTS (multiple of 8)
+ *   R      [M, K] bf16 or NULL, row stride ldr elements (multiple of 8)
+ *   gamma  [K] bf16
+ *   eps    >= 0
+ *   Rout   [M, K] bf16 or NULL, row stride ldo elements (multiple of 8); may
+ *          be R or X itself (same pointer and stride), otherwise disjoint
+ *   Q      codes as the quantiser's, row stride ldq bytes (multiple of 16)
+ *   scale  [M] fp32;  S [M, K/128] fp32 or [M, K/32] bytes, row stride lds
+ *          elements
+ * X, R, gamma, Rout, Q 16-byte aligned; fp32 scales 4-byte; K a positive
+ * multiple of 32 (f8_block: 128).  M == 0 is a no-op.  Inputs are finite: a
+ * row holding NaN or infinity gets unspecified codes and scales. */
+qgemm_status qgemm_rmsnorm_quant_i8_rowwise(const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                                            const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo,
+                                            int8_t *Q, int64_t ldq, float *scale, int64_t M, int64_t K,
+                                            void *stream);
+qgemm_status qgemm_rmsnorm_quant_f8_pertoken(const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                                             const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo,
+                                             uint8_t *Q, int64_t ldq, float *scale, int64_t M, int64_t K,
+                                             void *stream);
+qgemm_status qgemm_rmsnorm_quant_f8_block(const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                                          const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo,
+                                          uint8_t *Q, int64_t ldq, float *S, int64_t lds, int64_t M, int64_t K,
+                                          void *stream);
+qgemm_status qgemm_rmsnorm_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t ldx, const uint16_t *R,
+                                    int64_t ldr, const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo,
+                                    void *Q, int64_t ldq, uint8_t *S, int64_t lds, int64_t M, int64_t K,
+                                    void *stream);
+
 /* Text of the last non-OK status returned on the calling thread ("" if none). */
 const char *qgemm_last_error(void);
 
