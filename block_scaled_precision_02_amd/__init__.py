@@ -30,6 +30,10 @@ and the operators a decoder layer runs between its GEMMs (``layer.py``):
     qgemm_rmsnorm_quant_i8_rowwise / _f8_pertoken / _f8_block
         (X, gamma, eps=1e-6, residual=None, residual_out=None, out=None, scale=None)  -> (Q, scale, residual_out)
     qgemm_rmsnorm_quant_mx(fmt, X, gamma, ...)            -> (Q, S, residual_out)
+    KV8Cache(k, v, k_scale, v_scale) / KV8Cache.empty(...)   the paged 8-bit cache
+    qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q)
+    qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_kv, sm_scale=None, causal=True,
+                        window=0, out=None, workspace=None)  -> O
 
 Operands are [rows, K] with unit stride along K (row stride may exceed the
 row; it is passed as lda).  ``out`` may be a view of a wider buffer (row
@@ -56,6 +60,8 @@ QGEMM_MX_E2M3 = 2
 QGEMM_MX_E3M2 = 3
 QGEMM_MX_BSCALE_1x32 = 1
 QGEMM_MX_BSCALE_32x32 = 32
+QGEMM_KV8_E4M3 = 0
+QGEMM_KV8_I8 = 1
 
 # Every symbol include/qgemm.h declares.
 EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f8_blockscale", "qgemm_mx", "qgemm_mx_mixed",
@@ -64,7 +70,7 @@ EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f
            "qgemm_f8_pertoken_prepacked", "qgemm_f8_blockscale_prepacked", "qgemm_mx_prepacked",
            "qgemm_quant_f8_pertoken", "qgemm_quant_f8_block", "qgemm_quant_mx",
            "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_f8_block",
-           "qgemm_rmsnorm_quant_mx",
+           "qgemm_rmsnorm_quant_mx", "qgemm_kv8_append", "qgemm_kv8_attention", "qgemm_kv8_attention_workspace",
            "qgemm_last_error", "qgemm_status_string", "qgemm_select_tile",
            "qgemm_tile_rows", "qgemm_force_tile")
 
@@ -139,6 +145,13 @@ def declare(L):
     L.qgemm_rmsnorm_quant_f8_block.argtypes = norm + [_I64, _I64, _I64, _P]
     L.qgemm_rmsnorm_quant_mx.restype = st
     L.qgemm_rmsnorm_quant_mx.argtypes = [ctypes.c_int] + norm + [_I64, _I64, _I64, _P]
+    L.qgemm_kv8_append.restype = st
+    L.qgemm_kv8_append.argtypes = [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P]
+    L.qgemm_kv8_attention_workspace.restype = _I64
+    L.qgemm_kv8_attention_workspace.argtypes = [_P, _I64, _I64, _I64, _I64, _I64, ctypes.c_int, _I64]
+    L.qgemm_kv8_attention.restype = st
+    L.qgemm_kv8_attention.argtypes = [_P, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                                      ctypes.c_float, ctypes.c_int, _I64, _P, _I64, _P, _I64, _P]
     L.qgemm_last_error.restype = ctypes.c_char_p
     L.qgemm_last_error.argtypes = []
     L.qgemm_status_string.restype = ctypes.c_char_p
@@ -702,5 +715,5 @@ def qgemm_mx_prepacked(fmt, A, Bp, scale_a, scale_b, b_layout, bias=None, out=No
     return out
 
 
-from .layer import (qgemm_rmsnorm_quant_f8_block, qgemm_rmsnorm_quant_f8_pertoken,  # noqa: E402,F401
-                    qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx)
+from .layer import (KV8Cache, qgemm_kv8_append, qgemm_kv8_attention, qgemm_rmsnorm_quant_f8_block,  # noqa: E402,F401
+                    qgemm_rmsnorm_quant_f8_pertoken, qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx)

@@ -20,4 +20,36 @@ struct NormArgs {
 };
 hipError_t launch_rmsnorm_quant(int out, const NormArgs &a, hipStream_t s);
 
+// The paged 8-bit cache (kv8_dev.hpp has the layout).
+enum Kv8Fmt { KV8_E4M3 = 0, KV8_I8 = 1 };
+struct Kv8Append {
+    uint8_t *ck, *cv;
+    float *sk, *sv;                   // [blocks, kv_heads]
+    const uint16_t *K, *V;            // bf16 [tokens, kv_heads, dim], token strides ldk, ldv elements
+    const int32_t *table, *cu, *lens; // [batch, ldt], [batch + 1], [batch]
+    int64_t ldk, ldv, ldt, tokens;
+    int blocks, kv_heads, dim, bs, fmt, width, batch, max_q;
+};
+hipError_t launch_kv8_append(const Kv8Append &a, hipStream_t s);
+
+struct Kv8Attn {
+    const uint8_t *ck, *cv;
+    const float *sk, *sv;
+    const uint16_t *Q;                // bf16 [tokens, heads, dim], token stride ldq elements
+    uint16_t *O;                      // the same, ldo
+    const int32_t *table, *cu, *lens;
+    float *part, *stat;               // workspace of a split call
+    int64_t ldq, ldo, ldt, tokens;
+    float scale2;                     // softmax scale times log2(e)
+    int blocks, kv_heads, group, dim, bs, fmt, width, batch, max_q, max_kv, causal, window;
+    // the plan (kv8_plan)
+    int kernel;                       // 0 streaming (few rows), 1 tiled (many rows)
+    int nt;                           // streaming: 16-row tiles a wave
+    int row_tiles;                    // of the longest sequence, per kv head
+    int split_steps, splits;          // streaming: steps of 64 tokens a split, splits
+};
+// Fills the plan; returns the workspace bytes it needs.
+int64_t kv8_plan(Kv8Attn &a);
+hipError_t launch_kv8_attention(const Kv8Attn &a, hipStream_t s);
+
 }  // namespace qgemm

@@ -2,6 +2,8 @@
 // checks, then the launchers of layer.hpp.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "../qgemm_host.hpp"
 #include "layer.hpp"
 
@@ -61,6 +63,85 @@ qgemm_status norm_common(int out, const uint16_t *X, int64_t ldx, const uint16_t
     return launch([&] { return launch_rmsnorm_quant(out, a, (hipStream_t)stream); });
 }
 
+// ------------------------------------------------------------ 8-bit cache
+
+qgemm_status check_cache(const qgemm_kv8_cache *c)
+{
+    if (!c)
+        return fail(QGEMM_ERR_NULL_POINTER, "cache is NULL");
+    if (c->fmt != QGEMM_KV8_E4M3 && c->fmt != QGEMM_KV8_I8)
+        return fail(QGEMM_ERR_BAD_FORMAT, "unknown cache format %d", c->fmt);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256)
+        return fail(QGEMM_ERR_BAD_SHAPE, "head_dim=%d: need 64, 128, 192 or 256", c->head_dim);
+    if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
+        return fail(QGEMM_ERR_BAD_SHAPE, "block=%d tokens: need 16, 32, 64 or 128", c->block);
+    if (c->kv_heads <= 0 || c->kv_heads > 32767)
+        return fail(QGEMM_ERR_BAD_SHAPE, "kv_heads=%d: need 1 to 32767", c->kv_heads);
+    if (c->num_blocks <= 0 || c->num_blocks >= LD_LIMIT)
+        return fail(QGEMM_ERR_BAD_SHAPE, "num_blocks=%lld: need 1 to 2^31 - 1", (long long)c->num_blocks);
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale)
+        return fail(QGEMM_ERR_NULL_POINTER, "a cache array is NULL");
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return fail(QGEMM_ERR_BAD_LAYOUT, "cache codes must be 16-byte aligned, scales 4-byte");
+    return QGEMM_OK;
+}
+
+// Sequences: block table, new-token offsets, lengths.
+qgemm_status check_seqs(const int32_t *table, int64_t ldt, int64_t width, const int32_t *cu, const int32_t *lens,
+                        int64_t tokens, int64_t batch, int64_t max_q)
+{
+    if (batch < 0 || batch > 65535)
+        return fail(QGEMM_ERR_BAD_SHAPE, "batch=%lld: need 0 to 65535", (long long)batch);
+    if (tokens < 0 || tokens >= LD_LIMIT || max_q < 0 || max_q > tokens)
+        return fail(QGEMM_ERR_BAD_SHAPE, "tokens=%lld max_q=%lld: need 0 <= max_q <= tokens < 2^31", (long long)tokens,
+                    (long long)max_q);
+    if (width < 0 || width >= LD_LIMIT || ldt < width)
+        return fail(QGEMM_ERR_BAD_SHAPE, "block table rows of %lld entries, stride %lld: need 0 <= entries <= stride",
+                    (long long)width, (long long)ldt);
+    if (batch == 0 || max_q == 0)
+        return QGEMM_OK;
+    if (!table || !cu || !lens)
+        return fail(QGEMM_ERR_NULL_POINTER, "block_table, cu_seqlens or kv_lens is NULL");
+    if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4))
+        return fail(QGEMM_ERR_BAD_LAYOUT, "block_table, cu_seqlens and kv_lens must be 4-byte aligned");
+    return QGEMM_OK;
+}
+
+qgemm_status check_attn_shape(const qgemm_kv8_cache *c, int64_t heads, int64_t max_kv, int causal, int64_t window)
+{
+    if (heads <= 0 || heads % c->kv_heads || heads > 65535)
+        return fail(QGEMM_ERR_BAD_SHAPE, "heads=%lld: need a multiple of kv_heads=%d, at most 65535", (long long)heads,
+                    c->kv_heads);
+    if (max_kv < 0 || max_kv >= LD_LIMIT)
+        return fail(QGEMM_ERR_BAD_SHAPE, "max_kv=%lld: need 0 to 2^31 - 1", (long long)max_kv);
+    if (window < 0 || window >= LD_LIMIT || (window > 0 && !causal))
+        return fail(QGEMM_ERR_BAD_SHAPE, "window=%lld: need 0 (none) or a length, with causal", (long long)window);
+    return QGEMM_OK;
+}
+
+Kv8Attn attn_args(const qgemm_kv8_cache *c, int64_t tokens, int64_t batch, int64_t heads, int64_t max_q,
+                  int64_t max_kv, int causal, int64_t window)
+{
+    Kv8Attn a = {};
+    a.ck = (const uint8_t *)c->k;
+    a.cv = (const uint8_t *)c->v;
+    a.sk = c->k_scale;
+    a.sv = c->v_scale;
+    a.tokens = tokens;
+    a.blocks = (int)c->num_blocks;
+    a.kv_heads = c->kv_heads;
+    a.group = (int)(heads / c->kv_heads);
+    a.dim = c->head_dim;
+    a.bs = c->block;
+    a.fmt = c->fmt;
+    a.batch = (int)batch;
+    a.max_q = (int)max_q;
+    a.max_kv = (int)max_kv;
+    a.causal = causal != 0;
+    a.window = (int)window;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -94,6 +175,80 @@ qgemm_status qgemm_rmsnorm_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t
         return fail(QGEMM_ERR_BAD_FORMAT, "unknown MX element format %d", (int)fmt);
     return norm_common(fmt == QGEMM_MX_E4M3 ? NORM_MX_E4M3 : NORM_MX_E2M1, X, ldx, R, ldr, gamma, eps, Rout, ldo, Q,
                        ldq, S, lds, K / 32, M, K, stream);
+}
+
+qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, int64_t ldk, const uint16_t *V,
+                              int64_t ldv, const int32_t *block_table, int64_t ldt, int64_t width,
+                              const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t tokens, int64_t batch,
+                              int64_t max_q, void *stream)
+{
+    TRY(check_cache(cache));
+    TRY(check_seqs(block_table, ldt, width, cu_seqlens, kv_lens, tokens, batch, max_q));
+    if (batch == 0 || max_q == 0)
+        return QGEMM_OK;
+    const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+    TRY(check_rows("K", K, ldk, row));
+    TRY(check_rows("V", V, ldv, row));
+    TRY(check_device());
+    const Kv8Append a = {(uint8_t *)cache->k, (uint8_t *)cache->v, cache->k_scale, cache->v_scale, K, V, block_table,
+                         cu_seqlens, kv_lens, ldk, ldv, ldt, tokens, (int)cache->num_blocks, cache->kv_heads,
+                         cache->head_dim, cache->block, cache->fmt, (int)width, (int)batch, (int)max_q};
+    return launch([&] { return launch_kv8_append(a, (hipStream_t)stream); });
+}
+
+int64_t qgemm_kv8_attention_workspace(const qgemm_kv8_cache *cache, int64_t tokens, int64_t batch, int64_t heads,
+                                      int64_t max_q, int64_t max_kv, int causal, int64_t window)
+{
+    if (check_cache(cache) != QGEMM_OK || check_attn_shape(cache, heads, max_kv, causal, window) != QGEMM_OK ||
+        check_seqs(nullptr, 0, 0, nullptr, nullptr, tokens, 0, max_q) != QGEMM_OK || batch < 0 || batch > 65535)
+        return -1;
+    if (batch == 0 || max_q == 0)
+        return 0;
+    Kv8Attn a = attn_args(cache, tokens, batch, heads, max_q, max_kv, causal, window);
+    return kv8_plan(a);
+}
+
+qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q, int64_t ldq,
+                                 const int32_t *block_table, int64_t ldt, int64_t width, const int32_t *cu_seqlens,
+                                 const int32_t *kv_lens, int64_t tokens, int64_t batch, int64_t heads, int64_t max_q,
+                                 int64_t max_kv, float sm_scale, int causal, int64_t window, uint16_t *O, int64_t ldo,
+                                 void *workspace, int64_t workspace_bytes, void *stream)
+{
+    TRY(check_cache(cache));
+    TRY(check_seqs(block_table, ldt, width, cu_seqlens, kv_lens, tokens, batch, max_q));
+    TRY(check_attn_shape(cache, heads, max_kv, causal, window));
+    if (!std::isfinite(sm_scale))
+        return fail(QGEMM_ERR_BAD_SHAPE, "sm_scale is not finite");
+    if (batch == 0 || max_q == 0)
+        return QGEMM_OK;
+    TRY(check_rows("Q", Q, ldq, heads * cache->head_dim));
+    TRY(check_rows("O", O, ldo, heads * cache->head_dim));
+    Kv8Attn a = attn_args(cache, tokens, batch, heads, max_q, max_kv, causal, window);
+    const int64_t need = kv8_plan(a);
+    if (need > 0) {
+        if (!workspace)
+            return fail(QGEMM_ERR_NULL_POINTER, "workspace is NULL; this call needs %lld bytes", (long long)need);
+        if (!aligned(workspace, 16) || workspace_bytes < need)
+            return fail(QGEMM_ERR_BAD_LAYOUT, "workspace of %lld bytes: need %lld, 16-byte aligned",
+                        (long long)workspace_bytes, (long long)need);
+    }
+    if ((int64_t)a.row_tiles * a.splits * 256 >= (LD_LIMIT << 1) || max_q * 256 >= (LD_LIMIT << 1))
+        return fail(QGEMM_ERR_BAD_SHAPE, "max_q=%lld with %lld heads is too large for one call", (long long)max_q,
+                    (long long)heads);
+    TRY(check_device());
+    a.Q = Q;
+    a.O = O;
+    a.table = block_table;
+    a.cu = cu_seqlens;
+    a.lens = kv_lens;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.ldt = ldt;
+    a.width = (int)width;
+    a.scale2 = sm_scale * 1.44269504088896340736f;   // log2(e): the softmax runs on powers of two
+    a.part = (float *)workspace;
+    a.stat = a.part + (need > 0 ? tokens * heads * a.splits * a.dim : 0);
+    return launch([&] { return launch_kv8_attention(a, (hipStream_t)stream); });
 }
 
 }  // extern "C"

@@ -1,9 +1,11 @@
 """The operators that a decoder layer runs between its GEMMs: argument
 marshalling for the C entry points of the same names.  Errors as in the
 package: ValueError for arguments, RuntimeError for the device."""
+import ctypes
+
 import torch
 
-from . import (QGEMM_MX_E2M1, QGEMM_MX_E4M3, _check, _codes_out, _ld_bytes, _operand, _ptr, _same_device, _stream,
+from . import (QGEMM_KV8_E4M3, QGEMM_KV8_I8, QGEMM_MX_E2M1, QGEMM_MX_E4M3, _check, _codes_out, _ld_bytes, _operand, _ptr, _same_device, _stream,
                _vector, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
@@ -117,3 +119,139 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
                                             _ptr(residual_out), ldo, _ptr(out), _ld_bytes(out, row), _ptr(scale), lds,
                                             M, K, _stream(X.device, stream)))
     return out, scale, residual_out
+
+
+# ------------------------------------------------------------ 8-bit cache
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class KV8Cache:
+    """A paged cache of keys and values in 8 bits with one fp32 scale for each
+    block of tokens and kv head.
+
+        k        [blocks, kv_heads, block, head_dim]  int8, or e4m3 as
+                 float8_e4m3fn or uint8
+        v        [blocks, kv_heads, head_dim, block]  the same type
+        k_scale, v_scale   fp32 [blocks, kv_heads]
+
+    all contiguous on one device.  The cache holds the tensors; what is written
+    into them is seen by the next call."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError(f"{name} must be a contiguous tensor on a GPU device, the same for all four")
+        if k.dim() != 4 or k.dtype not in (torch.int8, torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise ValueError("k and v must be 4-D, both int8 or both e4m3 (float8_e4m3fn or uint8)")
+        blocks, heads, block, dim = k.shape
+        if tuple(v.shape) != (blocks, heads, dim, block):
+            raise ValueError(f"v must be {(blocks, heads, dim, block)} for k of {tuple(k.shape)}, got {tuple(v.shape)}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or tuple(t.shape) != (blocks, heads):
+                raise ValueError(f"{name} must be float32 {(blocks, heads)}, got {t.dtype} {tuple(t.shape)}")
+        if dim not in (64, 128, 192, 256) or block not in (16, 32, 64, 128):
+            raise ValueError(f"head_dim {dim} must be 64, 128, 192 or 256 and block {block} 16, 32, 64 or 128")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_blocks, self.kv_heads, self.block, self.head_dim = blocks, heads, block, dim
+        self.fmt = QGEMM_KV8_I8 if k.dtype == torch.int8 else QGEMM_KV8_E4M3
+        self.device = k.device
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), blocks, heads,
+                                    dim, block, self.fmt)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, num_blocks, kv_heads, head_dim, block=64, fmt=QGEMM_KV8_E4M3, device="cuda"):
+        """A cache with nothing in it (contents undefined until appended)."""
+        if fmt not in (QGEMM_KV8_E4M3, QGEMM_KV8_I8):
+            raise ValueError(f"unknown cache format {fmt}")
+        dtype = torch.int8 if fmt == QGEMM_KV8_I8 else torch.float8_e4m3fn
+        return cls(torch.empty((num_blocks, kv_heads, block, head_dim), dtype=dtype, device=device),
+                   torch.empty((num_blocks, kv_heads, head_dim, block), dtype=dtype, device=device),
+                   torch.empty((num_blocks, kv_heads), dtype=torch.float32, device=device),
+                   torch.empty((num_blocks, kv_heads), dtype=torch.float32, device=device))
+
+
+def _token_rows(t, name, heads, dim, device):
+    """Token stride (elements) of a [tokens, heads, dim] bf16 tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _BF16 or t.device != device:
+        raise ValueError(f"{name} must be a bfloat16 tensor on {device}")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(shape)}")
+    if st[2] != 1 or (shape[1] > 1 and st[1] != dim):
+        raise ValueError(f"{name} must have unit stride along its last axis and adjacent heads")
+    return st[0] if shape[0] > 1 else shape[1] * dim
+
+
+def _sequences(table, cu, lens, device):
+    batch = lens.shape[0]
+    for name, t in (("block_table", table), ("cu_seqlens", cu), ("kv_lens", lens)):
+        if t.dtype != torch.int32 or t.device != device:
+            raise ValueError(f"{name} must be int32 on {device}, got {t.dtype} on {t.device}")
+    if lens.dim() != 1 or cu.dim() != 1 or cu.shape[0] != batch + 1 or not lens.is_contiguous() \
+            or not cu.is_contiguous():
+        raise ValueError(f"kv_lens must be [batch] and cu_seqlens [batch + 1], contiguous; got {tuple(lens.shape)} and "
+                         f"{tuple(cu.shape)}")
+    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{batch}, blocks] with unit stride along its rows, got "
+                         f"{tuple(table.shape)}")
+    width = table.shape[1]
+    return batch, max(table.stride(0), width) if batch > 1 else width, width
+
+
+def qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q, stream=None):
+    """Append new tokens' keys and values to their sequences, quantised into
+    the cache in place.  K, V bf16 [tokens, kv_heads, head_dim] (token rows may
+    be slices of a wider row); block_table int32 [batch, blocks]; cu_seqlens
+    int32 [batch + 1] the offsets of each sequence's new tokens; kv_lens int32
+    [batch] the lengths with them; max_q at least the most new tokens of a
+    sequence."""
+    device = cache.device
+    ldk = _token_rows(K, "K", cache.kv_heads, cache.head_dim, device)
+    ldv = _token_rows(V, "V", cache.kv_heads, cache.head_dim, device)
+    tokens = K.shape[0]
+    if V.shape[0] != tokens:
+        raise ValueError(f"K holds {tokens} tokens, V {V.shape[0]}")
+    batch, ldt, width = _sequences(block_table, cu_seqlens, kv_lens, device)
+    with torch.cuda.device(device):
+        _check(lib().qgemm_kv8_append(cache._ref, _ptr(K), ldk, _ptr(V), ldv, _ptr(block_table), ldt, width,
+                                      _ptr(cu_seqlens), _ptr(kv_lens), tokens, batch, max_q, _stream(device, stream)))
+
+
+def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_kv, sm_scale=None, causal=True,
+                        window=0, out=None, workspace=None, stream=None):
+    """Attention of the new tokens (already appended) over the cache -> bf16
+    [tokens, heads, head_dim].  Q bf16 [tokens, heads, head_dim]; block_table,
+    cu_seqlens, kv_lens, max_q as for qgemm_kv8_append; max_kv at least the
+    longest kv_lens; sm_scale defaults to head_dim ** -0.5; window > 0 keeps
+    the last that many positions of each token.  workspace: a uint8 tensor of
+    at least qgemm_kv8_attention_workspace(...) bytes, allocated here if not
+    given.  Tokens of no sequence are left as they are in ``out``."""
+    device = cache.device
+    ldq = _token_rows(Q, "Q", None, cache.head_dim, device)
+    tokens, heads = Q.shape[0], Q.shape[1]
+    batch, ldt, width = _sequences(block_table, cu_seqlens, kv_lens, device)
+    if out is None:
+        out = torch.empty((tokens, heads, cache.head_dim), dtype=torch.bfloat16, device=device)
+    elif out.dtype != torch.bfloat16 or out.shape[0] != tokens:
+        raise ValueError(f"out must be bfloat16 [{tokens}, {heads}, {cache.head_dim}]")
+    ldo = _token_rows(out, "out", heads, cache.head_dim, device)
+    if sm_scale is None:
+        sm_scale = cache.head_dim ** -0.5
+    causal = 1 if causal else 0
+    if workspace is None:
+        need = lib().qgemm_kv8_attention_workspace(cache._ref, tokens, batch, heads, max_q, max_kv, causal, window)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with torch.cuda.device(device):
+        _check(lib().qgemm_kv8_attention(cache._ref, _ptr(Q), ldq, _ptr(block_table), ldt, width, _ptr(cu_seqlens),
+                                         _ptr(kv_lens), tokens, batch, heads, max_q, max_kv, sm_scale, causal, window,
+                                         _ptr(out), ldo, _ptr(workspace), nbytes, _stream(device, stream)))
+    return out

@@ -373,6 +373,88 @@ qgemm_status qgemm_rmsnorm_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t
                                     void *Q, int64_t ldq, uint8_t *S, int64_t lds, int64_t M, int64_t K,
                                     void *stream);
 
+/* A paged cache of keys and values in 8 bits, one fp32 scale for each block of
+ * tokens and kv head (K and V apart): the value of a code c is c * scale.
+ * A sequence's position p lives in physical block block_table[p / block], at
+ * place p % block.  All arrays are the caller's device memory; the struct
+ * itself is host memory read during the call.
+ *   k        codes [num_blocks, kv_heads, block, head_dim]
+ *   v        codes [num_blocks, kv_heads, head_dim, block]   (transposed: the
+ *            order in which the attention's second product takes them)
+ *   k_scale, v_scale   fp32 [num_blocks, kv_heads]
+ *   fmt      QGEMM_KV8_E4M3 (e4m3fn) or QGEMM_KV8_I8 (int8, -127 .. 127)
+ * head_dim 64, 128, 192 or 256; block 16, 32, 64 or 128 tokens; codes 16-byte
+ * aligned.  The cache may exceed 4 GiB. */
+typedef enum { QGEMM_KV8_E4M3 = 0, QGEMM_KV8_I8 = 1 } qgemm_kv8_fmt;
+typedef struct {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t num_blocks;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t block;
+    int32_t fmt;
+} qgemm_kv8_cache;
+
+/* Append new tokens' keys and values to their sequences.
+ *   K, V         [tokens, kv_heads, head_dim] bf16, token strides ldk, ldv
+ *                ELEMENTS (multiples of 8), heads adjacent, 16-byte aligned
+ *   block_table  [batch, width] int32, row stride ldt entries
+ *   cu_seqlens   [batch + 1] int32: sequence b's new tokens are rows
+ *                cu_seqlens[b] .. cu_seqlens[b+1]-1 of K and V
+ *   kv_lens      [batch] int32: sequence b's length WITH its new tokens, which
+ *                take the positions up to kv_lens[b]-1
+ *   max_q        at least the largest count of new tokens of a sequence
+ * For each block and head that new tokens touch, K and V apart, qmax = 448
+ * (e4m3) or 127 (int8):
+ *   s = fp32( amax(new) * fp32(1 / qmax) ), or the block's scale where it holds older
+ *       tokens of the sequence and that is larger
+ *   code = enc( fp32( x / s ) )       nearest, ties to even, saturating
+ *   where s exceeds the block's scale s0, its older codes c become
+ *       enc( fp32( fp32(c * s0) / s ) )
+ * (s = 0, all values zero: zero codes).  Codes at positions past kv_lens keep
+ * their bytes; a scale without older tokens is ignored and overwritten.  A
+ * block that several sequences share must not be touched by a call.  Tokens
+ * whose position is negative or whose block-table entry lies outside
+ * [0, num_blocks) or [0, width) are not stored.  Inputs are finite. */
+qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, int64_t ldk, const uint16_t *V,
+                              int64_t ldv, const int32_t *block_table, int64_t ldt, int64_t width,
+                              const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t tokens, int64_t batch,
+                              int64_t max_q, void *stream);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * already appended): for token t of sequence b's q new ones, at position
+ * P = kv_lens[b] - q + t, and query head h (kv head h / (heads / kv_heads)):
+ *   S[j] = sm_scale * sum_d Q[t,h,d] * K[j,d]      over the visible j:
+ *          0 <= j < kv_lens[b]; causal: j <= P; window > 0: j > P - window
+ *   O[t,h,:] = bf16( sum_j softmax(S)[j] * V[j,:] )
+ * A row that sees nothing gives zeros.  Products take Q and the codes
+ * exactly and the probabilities, times the block's V scale and relative to the
+ * row's largest, in binary16; maxima, sums and accumulators are binary32.  V
+ * scales below 2^-100 are read as 2^-100, zero as zero.  The result of a call does not depend on timing.
+ *   Q, O         [tokens, heads, head_dim] bf16, token strides ldq, ldo
+ *                elements (multiples of 8), heads adjacent, 16-byte aligned
+ *   block_table, cu_seqlens, kv_lens   as for the append
+ *   max_q, max_kv   at least the largest count of new tokens and the largest
+ *                kv_lens: tokens past them are not computed or not seen
+ *   window       0 for none; needs causal
+ *   workspace    qgemm_kv8_attention_workspace(...) bytes, 16-byte aligned
+ *                (may be NULL if that is 0); contents undefined before and
+ *                after; one call at a time
+ * Positions whose block-table entry lies outside [0, num_blocks) or past width
+ * count as not visible.  Nothing of a block is read past the rows' visible
+ * range that could reach the result: bytes there may hold anything, NaN codes
+ * included; visible codes are finite, visible scales finite and >= 0. */
+int64_t qgemm_kv8_attention_workspace(const qgemm_kv8_cache *cache, int64_t tokens, int64_t batch, int64_t heads,
+                                      int64_t max_q, int64_t max_kv, int causal, int64_t window);
+qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q, int64_t ldq,
+                                 const int32_t *block_table, int64_t ldt, int64_t width, const int32_t *cu_seqlens,
+                                 const int32_t *kv_lens, int64_t tokens, int64_t batch, int64_t heads, int64_t max_q,
+                                 int64_t max_kv, float sm_scale, int causal, int64_t window, uint16_t *O, int64_t ldo,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Text of the last non-OK status returned on the calling thread ("" if none). */
 const char *qgemm_last_error(void);
 

@@ -1,0 +1,348 @@
+"""GPU tests of the 8-bit cache: the append bit for bit against binary32 steps
+on the CPU, the attention against binary64 within the kernel's roundings;
+blocks, head counts, lengths, masks that leave rows empty, NaN in what is not
+seen, block-table entries out of range, caches past 4 GiB, other streams and
+replayed graphs."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import block_scaled_precision_02_amd as q  # noqa: E402
+
+from tests import kv8_ref  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _gpu_only():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+class Setup:
+    """Sequences with cached tokens, a shuffled block table and garbage in all
+    that no sequence holds."""
+
+    def __init__(self, fmt, kvh, dim, bs, seqs, seed=0, spare=2, poison=True):
+        rng = np.random.default_rng(seed)
+        self.fmt, self.kvh, self.dim, self.bs = fmt, kvh, dim, bs
+        self.cu = [0] + list(np.cumsum([s[0] for s in seqs]).tolist())
+        self.lens = [s[1] for s in seqs]
+        per = [max(0, -(-n // bs)) for n in self.lens]
+        blocks = max(1, sum(per) + spare)
+        order = rng.permutation(blocks)
+        width = max(per + [1])
+        self.table = np.full((len(seqs), width), -7, np.int64)        # what is not held is out of range
+        at = 0
+        for b, n in enumerate(per):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        codes = rng.standard_normal((2, blocks, kvh, bs, dim)).astype(np.float32)
+        k, v = codes[0], codes[1].swapaxes(2, 3).copy()
+        unit = np.float32(100.0 if fmt == "e4m3" else 30.0)
+        enc = lambda x: torch.from_numpy(kv8_ref.encode(x * unit, fmt)).view(kv8_ref.DTYPE[fmt])  # noqa: E731
+        self.cache = {"k": enc(k), "v": enc(v),
+                      "k_scale": torch.from_numpy((rng.uniform(0.5, 2, (blocks, kvh)) / unit).astype(np.float32)),
+                      "v_scale": torch.from_numpy((rng.uniform(0.5, 2, (blocks, kvh)) / unit).astype(np.float32))}
+        if poison:
+            held = set(order[:at].tolist())
+            bad = 0x7F if fmt == "e4m3" else 0x80
+            for i in range(blocks):
+                if i not in held:
+                    for n in ("k", "v"):
+                        self.cache[n][i].view(torch.uint8).fill_(bad)
+                        self.cache[n + "_scale"][i] = float("nan")
+            for b, n in enumerate(self.lens):
+                if n > 0 and n % bs:
+                    last = self.table[b, per[b] - 1]
+                    self.cache["k"][last, :, n % bs:].view(torch.uint8).fill_(bad)
+                    self.cache["v"][last].view(torch.uint8)[..., n % bs:] = bad
+        self.rng = rng
+
+    def gpu(self):
+        t = {n: x.cuda() for n, x in self.cache.items()}
+        return q.KV8Cache(t["k"], t["v"], t["k_scale"], t["v_scale"])
+
+    def seqs(self):
+        i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+        return i32(self.table), i32(self.cu), i32(self.lens)
+
+    def bf16(self, *shape):
+        return torch.from_numpy(self.rng.standard_normal(shape).astype(np.float32)).bfloat16()
+
+    @property
+    def tokens(self):
+        return self.cu[-1]
+
+    @property
+    def max_q(self):
+        return max(b - a for a, b in zip(self.cu, self.cu[1:]))
+
+    @property
+    def max_kv(self):
+        return max(max(self.lens), 0)
+
+
+def _attend(s, heads, causal=True, window=0, wide=0, **kw):
+    Q = s.bf16(s.tokens, heads, s.dim)
+    dev = Q.cuda()
+    if wide:
+        buf = torch.full((s.tokens, heads * s.dim + wide), float("nan"), dtype=torch.bfloat16, device="cuda")
+        buf[:, :heads * s.dim] = dev.view(s.tokens, -1)
+        dev = buf[:, :heads * s.dim].view(s.tokens, heads, s.dim)
+    table, cu, lens = s.seqs()
+    out = q.qgemm_kv8_attention(s.gpu(), dev, table, cu, lens, s.max_q, s.max_kv, causal=causal, window=window, **kw)
+    torch.cuda.synchronize()
+    want, tol = kv8_ref.attention(s.cache, Q, s.table.tolist(), s.cu, s.lens, s.fmt, causal, window,
+                                  kw.get("sm_scale"))
+    got = out.float().double().cpu().numpy()
+    assert np.isfinite(got).all()
+    off = np.abs(got - want) - tol
+    assert off.max() <= 0, (off.max(), np.unravel_index(off.argmax(), off.shape))
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_single_tokens(fmt, dim, bs):
+    s = Setup(fmt, 2, dim, bs, [(1, 1), (1, 63), (1, 64), (1, 65), (1, 200), (1, 1023)], seed=dim + bs)
+    _attend(s, 8)
+
+
+@pytest.mark.parametrize("kvh,heads", [(1, 1), (1, 16), (2, 34), (3, 9), (1, 40), (8, 8)])
+def test_shared_heads(kvh, heads):
+    s = Setup("e4m3", kvh, 128, 64, [(1, 500), (2, 77), (3, 130)], seed=heads)
+    _attend(s, heads)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_tokens(fmt, causal):
+    s = Setup(fmt, 2, 128, 32, [(5, 300), (1, 4), (7, 7), (2, 129)], seed=3)
+    _attend(s, 10, causal=causal)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts(fmt, dim, causal):
+    s = Setup(fmt, 1, dim, 64, [(70, 70), (130, 300), (1, 400), (257, 321)], seed=dim)
+    _attend(s, 4, causal=causal)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 128])
+def test_prompt_blocks(bs):
+    s = Setup("e4m3", 2, 128, bs, [(99, 99), (200, 555), (64, 64)], seed=bs)
+    _attend(s, 6)
+
+
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 5000])
+@pytest.mark.parametrize("seqs", [[(1, 700), (1, 3)], [(4, 333), (2, 64)], [(150, 400), (90, 91)]])
+def test_window(window, seqs):
+    s = Setup("e4m3", 2, 64, 32, seqs, seed=window)
+    # blocks wholly before every window are dropped: their places hold garbage
+    for b, n in enumerate(s.lens):
+        first = max(0, n - (s.cu[b + 1] - s.cu[b]) + 1 - window) // s.bs
+        for j in range(first):
+            blk = s.table[b, j]
+            s.cache["v"][blk].view(torch.uint8).fill_(0x7F)
+            s.cache["k"][blk].view(torch.uint8).fill_(0x7F)
+            s.cache["k_scale"][blk] = float("nan")
+            s.cache["v_scale"][blk] = float("inf")
+            s.table[b, j] = -1 if j % 2 else blk
+    _attend(s, 8, window=window)
+
+
+@pytest.mark.parametrize("q_over", [1, 40, 300])
+def test_rows_that_see_nothing(q_over):
+    """More new tokens than the sequence holds, empty sequences, a sequence
+    with no new tokens."""
+    s = Setup("i8", 2, 64, 16, [(q_over + 3, 3), (2, 0), (0, 50), (1, 20)], seed=q_over)
+    out = _attend(s, 4)
+    assert not bool(out[:q_over].any()) and not bool(out[q_over + 3:q_over + 5].any())
+    _attend(s, 4, causal=False)
+
+
+def test_missing_blocks_are_not_seen():
+    s = Setup("e4m3", 1, 128, 64, [(1, 640), (130, 640)], seed=5)
+    s.table[:, 3] = 10 ** 6
+    s.table[:, 4] = -1
+    _attend(s, 8)
+
+
+@pytest.mark.parametrize("batch,n,heads,kvh", [(1, 5000, 8, 1), (2, 3001, 16, 2), (1, 20000, 4, 1)])
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_long_caches_are_split(batch, n, heads, kvh, fmt):
+    s = Setup(fmt, kvh, 128, 64, [(1, n - 13 * b) for b in range(batch)], seed=n)
+    table, cu, lens = s.seqs()
+    assert q.lib().qgemm_kv8_attention_workspace(s.gpu()._ref, batch, batch, heads, 1, n, 1, 0) > 0
+    a = _attend(s, heads, wide=24)
+    s2 = Setup(fmt, kvh, 128, 64, [(1, n - 13 * b) for b in range(batch)], seed=n)
+    assert torch.equal(a.view(torch.int16), _attend(s2, heads).view(torch.int16))
+
+
+def test_large_scores_and_one_dominant_key():
+    s = Setup("e4m3", 1, 128, 64, [(1, 300), (40, 300)], seed=9)
+    s.cache["k_scale"][:] *= 40.0
+    s.cache["v_scale"][::2] *= 1e4
+    _attend(s, 4)
+    s.cache["v_scale"][:] = 0.0
+    s.cache["k_scale"][1::2] = 0.0
+    _attend(s, 4, sm_scale=-0.3)
+
+
+def test_strided_rows_and_out():
+    s = Setup("e4m3", 2, 64, 16, [(3, 100), (1, 33)], seed=4)
+    buf = torch.full((s.tokens, 8 * 64 + 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = _attend(s, 8, wide=16, out=buf[:, :512].view(s.tokens, 8, 64))
+    assert out.data_ptr() == buf.data_ptr() and bool((buf[:, 512:] == 7.0).all())
+
+
+@pytest.mark.parametrize("seqs", [[(1, 4000), (1, 77)], [(200, 500), (31, 64)]])
+def test_another_stream_and_graph(seqs):
+    s = Setup("e4m3", 2, 128, 64, seqs, seed=8)
+    cache, Q = s.gpu(), s.bf16(s.tokens, 8, 128).cuda()
+    table, cu, lens = s.seqs()
+    args = (table, cu, lens, s.max_q, s.max_kv)
+    want = q.qgemm_kv8_attention(cache, Q, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = q.qgemm_kv8_attention(cache, Q, *args)
+    side.synchronize()
+    assert torch.equal(want.view(torch.int16), again.view(torch.int16))
+    need = q.lib().qgemm_kv8_attention_workspace(cache._ref, s.tokens, len(seqs), 8, s.max_q, s.max_kv, 1, 0)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.qgemm_kv8_attention(cache, Q, *args, out=out, workspace=ws)
+    for _ in range(3):
+        Q.mul_(0.5)
+        want = q.qgemm_kv8_attention(cache, Q, *args)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want.view(torch.int16), out.view(torch.int16))
+
+
+def test_cache_past_4_gib():
+    """Blocks whose code offsets pass 2^32 and 2^33 bytes."""
+    blocks, kvh, bs, dim = 140000, 4, 128, 128
+    cache = q.KV8Cache.empty(blocks, kvh, dim, bs)
+    assert cache.k.numel() > 1 << 33
+    s = Setup("e4m3", kvh, dim, bs, [(1, 300), (140, 500)], seed=2, spare=0, poison=False)
+    ids = torch.tensor([0, 139999, 66000, 70001, 139000, 131072, 3], device="cuda")
+    assert len(ids) == s.cache["k"].shape[0]
+    for n in ("k", "v", "k_scale", "v_scale"):
+        dst = getattr(cache, n)
+        dst.view(torch.uint8 if dst.dtype != torch.float32 else dst.dtype)[ids] = \
+            s.cache[n].view(torch.uint8 if dst.dtype != torch.float32 else dst.dtype).cuda()
+    _, cu, lens = s.seqs()
+    far = torch.where(torch.tensor(s.table) >= 0, ids.cpu()[torch.tensor(s.table).clamp(min=0)], -1).int().cuda()
+    Q = s.bf16(s.tokens, 8, dim)
+    out = q.qgemm_kv8_attention(cache, Q.cuda(), far, cu, lens, s.max_q, s.max_kv)
+    want, tol = kv8_ref.attention(s.cache, Q, s.table.tolist(), s.cu, s.lens, "e4m3")
+    assert (np.abs(out.float().double().cpu().numpy() - want) <= tol).all()
+    # and the append into the same blocks
+    k, v = s.bf16(s.tokens, kvh, dim), s.bf16(s.tokens, kvh, dim)
+    q.qgemm_kv8_append(cache, k.cuda(), v.cuda(), far, cu, lens, s.max_q)
+    kv8_ref.append(s.cache, k, v, s.table.tolist(), s.cu, s.lens, "e4m3")
+    for n in ("k", "v"):
+        assert torch.equal(getattr(cache, n).view(torch.uint8)[ids].cpu(), s.cache[n].view(torch.uint8)), n
+
+
+# ------------------------------------------------------------ append
+
+def _append(s, factor=1.0, strided=False):
+    k, v = s.bf16(s.tokens, s.kvh, s.dim) * factor, s.bf16(s.tokens, s.kvh, s.dim) * factor
+    cache = s.gpu()
+    table, cu, lens = s.seqs()
+    dk, dv = k.cuda(), v.cuda()
+    if strided:
+        both = torch.cat([dk.view(s.tokens, -1), dv.view(s.tokens, -1)], 1)
+        dk, dv = (x.view(s.tokens, s.kvh, s.dim) for x in both.split(s.kvh * s.dim, 1))
+    q.qgemm_kv8_append(cache, dk, dv, table, cu, lens, s.max_q)
+    torch.cuda.synchronize()
+    kv8_ref.append(s.cache, k, v, s.table.tolist(), s.cu, s.lens, s.fmt)
+    for n in ("k", "v"):
+        got, want = getattr(cache, n).view(torch.uint8).cpu(), s.cache[n].view(torch.uint8)
+        assert torch.equal(got, want), (n, torch.nonzero(got != want)[:4])
+        got, want = getattr(cache, n + "_scale").cpu().view(torch.int32), s.cache[n + "_scale"].view(torch.int32)
+        assert torch.equal(got, want), n
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_append(fmt, dim, bs):
+    seqs = [(1, 1), (1, bs), (1, bs + 1), (1, 2 * bs - 3), (5, bs + 2), (3 * bs + 7, 4 * bs + 1), (2 * bs, 2 * bs)]
+    for factor in (0.1, 1.0, 30.0):        # scales that stay, and that grow and requantise the block
+        _append(Setup(fmt, 3, dim, bs, seqs, seed=bs + dim), factor, strided=factor == 1.0)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_append_edges(fmt):
+    seqs = [(0, 40), (9, 4), (2, 0), (6, 150), (4, 64)]
+    s = Setup(fmt, 2, 128, 64, seqs, seed=1)
+    s.table[3, 1] = 1 << 20                     # an entry out of range: not stored
+    _append(s)
+    for factor in (0.0, 2.0 ** -110, 2.0 ** 100):
+        _append(Setup(fmt, 2, 64, 16, [(3, 21), (1, 8), (40, 50)], seed=7), factor)
+
+
+def test_append_again_changes_nothing():
+    s = Setup("e4m3", 2, 128, 64, [(3, 70), (1, 9)], seed=6)
+    k, v = (s.bf16(s.tokens, 2, 128) * 20).cuda(), s.bf16(s.tokens, 2, 128).cuda()
+    cache = s.gpu()
+    table, cu, lens = s.seqs()
+    q.qgemm_kv8_append(cache, k, v, table, cu, lens, s.max_q)
+    first = [x.clone().view(torch.uint8) for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    q.qgemm_kv8_append(cache, k, v, table, cu, lens, s.max_q)
+    for a, b in zip(first, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+        assert torch.equal(a, b.view(torch.uint8))
+
+
+def test_append_then_attend_token_by_token():
+    """A prompt and then single tokens: the attention over what the appends
+    left equals the plain one over the same codes."""
+    s = Setup("i8", 2, 64, 16, [(37, 37), (5, 5)], seed=12)
+    cache = s.gpu()
+    wide = np.full((2, 8), -1, np.int64)
+    wide[0], wide[1] = np.arange(8), np.arange(8) + 8
+    cache = q.KV8Cache.empty(16, 2, 64, 16, q.QGEMM_KV8_I8)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    table = i32(wide)
+    lens = [0, 0]
+    for new in ([37, 5], [1, 1], [1, 3], [20, 1], [1, 1]):
+        lens = [a + b for a, b in zip(lens, new)]
+        cu = [0, new[0], new[0] + new[1]]
+        k, v, Q = s.bf16(cu[2], 2, 64), s.bf16(cu[2], 2, 64), s.bf16(cu[2], 8, 64)
+        q.qgemm_kv8_append(cache, k.cuda(), v.cuda(), table, i32(cu), i32(lens), max(new))
+        out = q.qgemm_kv8_attention(cache, Q.cuda(), table, i32(cu), i32(lens), max(new), max(lens))
+        held = {n: getattr(cache, n).cpu() for n in ("k", "v", "k_scale", "v_scale")}
+        want, tol = kv8_ref.attention(held, Q, wide.tolist(), cu, lens, "i8")
+        assert (np.abs(out.float().double().cpu().numpy() - want) <= tol).all()
+
+
+def test_python_refusals():
+    s = Setup("e4m3", 2, 64, 16, [(3, 20)], seed=1)
+    cache = s.gpu()
+    table, cu, lens = s.seqs()
+    Q = s.bf16(3, 4, 64).cuda()
+    ok = dict(block_table=table, cu_seqlens=cu, kv_lens=lens, max_q=3, max_kv=20)
+    for bad in (dict(ok, block_table=table.long()), dict(ok, cu_seqlens=cu[:1]), dict(ok, kv_lens=lens.cpu()),
+                dict(ok, max_q=-1), dict(ok, max_kv=-1), dict(ok, window=4, causal=False), dict(ok, max_q=4)):
+        with pytest.raises(ValueError):
+            q.qgemm_kv8_attention(cache, Q, **bad)
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_attention(cache, Q.float(), **ok)
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_attention(cache, Q[:, :3].contiguous(), **ok)          # 3 heads over 2
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_attention(cache, Q[:, :, :32], **ok)
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_append(cache, Q, Q, table, cu, lens, 3)               # 4 heads into 2
+    with pytest.raises(ValueError):
+        q.KV8Cache(cache.k, cache.v.transpose(2, 3).contiguous(), cache.k_scale, cache.v_scale)
