@@ -34,6 +34,8 @@ and the operators a decoder layer runs between its GEMMs (``layer.py``):
     qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q)
     qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_kv, sm_scale=None, causal=True,
                         window=0, out=None, workspace=None)  -> O
+    qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None)
+    qgemm_w4_matvec_mx(X, W, scale_b, b_layout, bias=None, out=None)
 
 Operands are [rows, K] with unit stride along K (row stride may exceed the
 row; it is passed as lda).  ``out`` may be a view of a wider buffer (row
@@ -71,6 +73,7 @@ EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f
            "qgemm_quant_f8_pertoken", "qgemm_quant_f8_block", "qgemm_quant_mx",
            "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_f8_block",
            "qgemm_rmsnorm_quant_mx", "qgemm_kv8_append", "qgemm_kv8_attention", "qgemm_kv8_attention_workspace",
+           "qgemm_w4_matvec_i4", "qgemm_w4_matvec_mx",
            "qgemm_last_error", "qgemm_status_string", "qgemm_select_tile",
            "qgemm_tile_rows", "qgemm_force_tile")
 
@@ -152,6 +155,10 @@ def declare(L):
     L.qgemm_kv8_attention.restype = st
     L.qgemm_kv8_attention.argtypes = [_P, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64,
                                       ctypes.c_float, ctypes.c_int, _I64, _P, _I64, _P, _I64, _P]
+    L.qgemm_w4_matvec_i4.restype = st
+    L.qgemm_w4_matvec_i4.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P]
+    L.qgemm_w4_matvec_mx.restype = st
+    L.qgemm_w4_matvec_mx.argtypes = [_P, _I64, _P, _I64, _P, ctypes.c_int, _P, _P, _I64, _I64, _I64, _I64, _P]
     L.qgemm_last_error.restype = ctypes.c_char_p
     L.qgemm_last_error.argtypes = []
     L.qgemm_status_string.restype = ctypes.c_char_p
@@ -716,4 +723,5 @@ def qgemm_mx_prepacked(fmt, A, Bp, scale_a, scale_b, b_layout, bias=None, out=No
 
 
 from .layer import (KV8Cache, qgemm_kv8_append, qgemm_kv8_attention, qgemm_rmsnorm_quant_f8_block,  # noqa: E402,F401
-                    qgemm_rmsnorm_quant_f8_pertoken, qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx)
+                    qgemm_rmsnorm_quant_f8_pertoken, qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx,
+                    qgemm_w4_matvec_i4, qgemm_w4_matvec_mx)

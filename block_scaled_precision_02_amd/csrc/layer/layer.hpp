@@ -52,4 +52,17 @@ struct Kv8Attn {
 int64_t kv8_plan(Kv8Attn &a);
 hipError_t launch_kv8_attention(const Kv8Attn &a, hipStream_t s);
 
+// bf16 rows times 4-bit weights (M <= 64).
+struct W4Args {
+    const uint16_t *X;                // bf16 [M, K], row stride ldx elements
+    const uint8_t *W;                 // [N, K/2] bytes, row stride ldw
+    const void *S;                    // bf16 [N, K/group], or ue8m0 [N / srows, K/32]
+    const uint8_t *Z;                 // [N, K/group] or NULL
+    const uint16_t *bias;             // bf16 [N] or NULL
+    uint16_t *Y;                      // bf16 [M, N], row stride ldy elements
+    int64_t ldx, ldw, ldy;
+    int M, N, K, group, srows;        // group 0: MX
+};
+hipError_t launch_w4_matvec(const W4Args &a, hipStream_t s);
+
 }  // namespace qgemm

@@ -142,6 +142,41 @@ Kv8Attn attn_args(const qgemm_kv8_cache *c, int64_t tokens, int64_t batch, int64
     return a;
 }
 
+// ------------------------------------------------------------ 4-bit matvec
+
+constexpr int64_t W4_MAX_M = 64;
+
+qgemm_status w4_common(W4Args a, int64_t M, int64_t N, int64_t K, int64_t group, void *stream)
+{
+    if (M < 0 || N < 0 || K <= 0 || M > W4_MAX_M || N >= LD_LIMIT || K >= LD_LIMIT)
+        return fail(QGEMM_ERR_BAD_SHAPE, "M=%lld N=%lld K=%lld: need 0 <= M <= %lld, 0 <= N < 2^31, 0 < K < 2^31",
+                    (long long)M, (long long)N, (long long)K, (long long)W4_MAX_M);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(QGEMM_ERR_BAD_SHAPE, "group=%lld: need 32, 64 or 128", (long long)group);
+    if (K % group)
+        return fail(QGEMM_ERR_BAD_SHAPE, "K=%lld is not a multiple of %lld", (long long)K, (long long)group);
+    if (M == 0 || N == 0)
+        return QGEMM_OK;
+    TRY(check_rows("X", a.X, a.ldx, K));
+    if (!a.W || !a.S || !a.Y)
+        return fail(QGEMM_ERR_NULL_POINTER, "%s is NULL", !a.W ? "W" : !a.S ? "the scale array" : "Y");
+    if (!aligned(a.W, 16) || a.ldw < K / 2 || a.ldw % 16 || a.ldw >= LD_LIMIT)
+        return fail(QGEMM_ERR_BAD_LAYOUT,
+                    "W must be 16-byte aligned with ldw=%lld bytes >= %lld, a multiple of 16, below 2^31",
+                    (long long)a.ldw, (long long)(K / 2));
+    if (a.group && !aligned(a.S, 2))
+        return fail(QGEMM_ERR_BAD_LAYOUT, "the scale array is not 2-byte aligned");
+    if (!aligned(a.bias, 2) || !aligned(a.Y, 2))
+        return fail(QGEMM_ERR_BAD_LAYOUT, "bias and Y must be 2-byte aligned");
+    if (a.ldy < N || a.ldy >= LD_LIMIT)
+        return fail(QGEMM_ERR_BAD_LAYOUT, "ldy=%lld: need >= N=%lld, below 2^31", (long long)a.ldy, (long long)N);
+    TRY(check_device());
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    return launch([&] { return launch_w4_matvec(a, (hipStream_t)stream); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -249,6 +284,44 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
     a.part = (float *)workspace;
     a.stat = a.part + (need > 0 ? tokens * heads * a.splits * a.dim : 0);
     return launch([&] { return launch_kv8_attention(a, (hipStream_t)stream); });
+}
+
+qgemm_status qgemm_w4_matvec_i4(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw, const uint16_t *scales,
+                                const uint8_t *zeros, int64_t group, const uint16_t *bias, uint16_t *Y, int64_t ldy,
+                                int64_t M, int64_t N, int64_t K, void *stream)
+{
+    W4Args a = {};
+    a.X = X;
+    a.W = W;
+    a.S = scales;
+    a.Z = zeros;
+    a.bias = bias;
+    a.Y = Y;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.ldy = ldy;
+    a.group = (int)group;
+    return w4_common(a, M, N, K, group, stream);
+}
+
+qgemm_status qgemm_w4_matvec_mx(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw, const uint8_t *scale_b,
+                                qgemm_mx_bscale b_layout, const uint16_t *bias, uint16_t *Y, int64_t ldy, int64_t M,
+                                int64_t N, int64_t K, void *stream)
+{
+    if (b_layout != QGEMM_MX_BSCALE_1x32 && b_layout != QGEMM_MX_BSCALE_32x32)
+        return fail(QGEMM_ERR_BAD_FORMAT, "unknown B-scale layout %d", (int)b_layout);
+    W4Args a = {};
+    a.X = X;
+    a.W = W;
+    a.S = scale_b;
+    a.bias = bias;
+    a.Y = Y;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.ldy = ldy;
+    a.group = 0;
+    a.srows = (int)b_layout;
+    return w4_common(a, M, N, K, 32, stream);
 }
 
 }  // extern "C"

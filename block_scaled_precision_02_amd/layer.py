@@ -255,3 +255,59 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
                                          _ptr(kv_lens), tokens, batch, heads, max_q, max_kv, sm_scale, causal, window,
                                          _ptr(out), ldo, _ptr(workspace), nbytes, _stream(device, stream)))
     return out
+
+
+# ------------------------------------------------------------ 4-bit matvec
+
+def _w4_args(X, W, bias, out):
+    ldx = _operand(X, "X", _BF16) // 2
+    ldw = _operand(W, "W", (torch.uint8,))
+    M, K = X.shape
+    N = W.shape[0]
+    if W.shape[1] * 2 != K:
+        raise ValueError(f"X is [M, K={K}] but W holds {2 * W.shape[1]} weights a row")
+    device = X.device
+    _vector(bias, "bias", N, _BF16)
+    _same_device(device, W, bias)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+    elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or out.device != device
+          or (N > 1 and out.stride(1) != 1)):
+        raise ValueError(f"out must be bfloat16 [{M}, {N}] with unit stride along N on {device}")
+    return ldx, ldw if N > 1 else ldw + (-ldw) % 16, M, N, K, out, out.stride(0) if M > 1 else N
+
+
+def _w4_table(t, name, shape, dtypes, device):
+    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be {dtypes} {shape}, contiguous, on {device}")
+
+
+def qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None, stream=None):
+    """bf16 X [M, K] (M <= 64) times int4 weights W uint8 [N, K/2] with bf16
+    scales and uint8 zero points (8 where None) per group: both
+    [N, K/group], group 32, 64 or 128 -> bf16 [M, N]."""
+    ldx, ldw, M, N, K, out, ldy = _w4_args(X, W, bias, out)
+    groups = scales.shape[1] if scales.dim() == 2 else 0
+    if groups == 0 or K % groups:
+        raise ValueError(f"scales must be [{N}, K/group], got {tuple(scales.shape)} for K={K}")
+    _w4_table(scales, "scales", (N, groups), _BF16, X.device)
+    if zeros is not None:
+        _w4_table(zeros, "zeros", (N, groups), (torch.uint8,), X.device)
+    with torch.cuda.device(X.device):
+        _check(lib().qgemm_w4_matvec_i4(_ptr(X), ldx, _ptr(W), ldw, _ptr(scales), _ptr(zeros), K // groups, _ptr(bias),
+                                        _ptr(out), ldy, M, N, K, _stream(X.device, stream)))
+    return out
+
+
+def qgemm_w4_matvec_mx(X, W, scale_b, b_layout, bias=None, out=None, stream=None):
+    """bf16 X [M, K] (M <= 64) times the MXFP4 B operand of qgemm_mx: W uint8
+    [N, K/2] e2m1, scale_b ue8m0 [N, K/32] (b_layout 1) or [ceil(N/32), K/32]
+    (b_layout 32) -> bf16 [M, N]."""
+    ldx, ldw, M, N, K, out, ldy = _w4_args(X, W, bias, out)
+    rows = -(-N // b_layout) if b_layout in (1, 32) else N
+    sdt = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+    _w4_table(scale_b, "scale_b", (rows, K // 32), sdt, X.device)
+    with torch.cuda.device(X.device):
+        _check(lib().qgemm_w4_matvec_mx(_ptr(X), ldx, _ptr(W), ldw, _ptr(scale_b), b_layout, _ptr(bias), _ptr(out),
+                                        ldy, M, N, K, _stream(X.device, stream)))
+    return out

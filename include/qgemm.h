@@ -455,6 +455,32 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
                                  int64_t max_kv, float sm_scale, int causal, int64_t window, uint16_t *O, int64_t ldo,
                                  void *workspace, int64_t workspace_bytes, void *stream);
 
+/* A few rows of bf16 activations times 4-bit weights, for the projections of
+ * decode steps (at most 64 rows; more rows: the GEMMs above).
+ *   X       [M, K] bf16, 0 <= M <= 64, row stride ldx elements (multiple of 8),
+ *           16-byte aligned
+ *   W       [N, K/2] bytes, weight k (k even) in bits 3:0 of byte k/2, k+1 in
+ *           bits 7:4; row stride ldw bytes (multiple of 16), 16-byte aligned
+ *   Y       [M, N] bf16, row stride ldy elements (>= N)
+ *   bias    [N] bf16 or NULL
+ * i4: unsigned 4-bit w with a scale and a zero point per group of 32, 64 or
+ *   128 elements of a row,
+ *     Y = bf16( sum_k X[m,k] * (w[n,k] - zero[n,k/group]) * scale[n,k/group] + bias[n] )
+ *   scales [N, K/group] bf16, zeros [N, K/group] bytes or NULL (8 everywhere)
+ * mx: the MXFP4 B operand of qgemm_mx as it is (e2m1, ue8m0 scale per 32
+ *   elements, [N, K/32] or [ceil(N/32), K/32] by b_layout); the activations
+ *   stay bf16.  Scale code 255 is NaN; an element times its scale has to lie
+ *   within bf16.
+ * Weights and X enter the products exactly, sums are binary32 in an order
+ * that depends on the shape alone.  Any N; K a positive multiple of the group
+ * (mx: 32). */
+qgemm_status qgemm_w4_matvec_i4(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw,
+                                const uint16_t *scales, const uint8_t *zeros, int64_t group, const uint16_t *bias,
+                                uint16_t *Y, int64_t ldy, int64_t M, int64_t N, int64_t K, void *stream);
+qgemm_status qgemm_w4_matvec_mx(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw,
+                                const uint8_t *scale_b, qgemm_mx_bscale b_layout, const uint16_t *bias, uint16_t *Y,
+                                int64_t ldy, int64_t M, int64_t N, int64_t K, void *stream);
+
 /* Text of the last non-OK status returned on the calling thread ("" if none). */
 const char *qgemm_last_error(void);
 

@@ -147,3 +147,41 @@ def test_attention_workspace():
     assert size(None, 1, 1, 8, 1, 100, 1, 0) == -1
     assert size(c.byref(k), 1, 1, 7, 1, 100, 1, 0) == -1
     assert size(c.byref(k), 1, 1, 8, 2, 100, 1, 0) == -1
+
+
+# ------------------------------------------------------------ 4-bit matvec
+
+def i4(X=A, ldx=256, W=B, ldw=128, S=C, Z=D, group=64, bias=E, Y=E, ldy=32, M=2, N=32, K=256):
+    return q.lib().qgemm_w4_matvec_i4(X, ldx, W, ldw, S, Z, group, bias, Y, ldy, M, N, K, None)
+
+
+def mx(X=A, ldx=256, W=B, ldw=128, S=C, layout=1, bias=E, Y=E, ldy=32, M=2, N=32, K=256):
+    return q.lib().qgemm_w4_matvec_mx(X, ldx, W, ldw, S, layout, bias, Y, ldy, M, N, K, None)
+
+
+@pytest.mark.parametrize("f", [i4, mx])
+@pytest.mark.parametrize("kw,status", [
+    (dict(X=None), q.QGEMM_ERR_NULL_POINTER), (dict(W=None), q.QGEMM_ERR_NULL_POINTER),
+    (dict(S=None), q.QGEMM_ERR_NULL_POINTER), (dict(Y=None), q.QGEMM_ERR_NULL_POINTER),
+    (dict(M=-1), q.QGEMM_ERR_BAD_SHAPE), (dict(M=65), q.QGEMM_ERR_BAD_SHAPE), (dict(N=-1), q.QGEMM_ERR_BAD_SHAPE),
+    (dict(K=0), q.QGEMM_ERR_BAD_SHAPE), (dict(K=240), q.QGEMM_ERR_BAD_SHAPE), (dict(N=1 << 31), q.QGEMM_ERR_BAD_SHAPE),
+    (dict(X=A + 8), q.QGEMM_ERR_BAD_LAYOUT), (dict(ldx=252), q.QGEMM_ERR_BAD_LAYOUT),
+    (dict(W=B + 4), q.QGEMM_ERR_BAD_LAYOUT), (dict(ldw=112), q.QGEMM_ERR_BAD_LAYOUT),
+    (dict(ldw=136), q.QGEMM_ERR_BAD_LAYOUT), (dict(bias=E + 1), q.QGEMM_ERR_BAD_LAYOUT),
+    (dict(Y=E + 1), q.QGEMM_ERR_BAD_LAYOUT), (dict(ldy=31), q.QGEMM_ERR_BAD_LAYOUT)])
+def test_matvec_refusals(f, kw, status):
+    assert f(**kw) == status
+
+
+def test_matvec_refusals_by_kind_empty_and_device(monkeypatch):
+    assert i4(group=16) == q.QGEMM_ERR_BAD_SHAPE and i4(group=0) == q.QGEMM_ERR_BAD_SHAPE
+    assert i4(S=C + 1) == q.QGEMM_ERR_BAD_LAYOUT
+    assert mx(layout=2) == q.QGEMM_ERR_BAD_FORMAT
+    for f in (i4, mx):
+        assert f(M=0, X=None, W=None, S=None, Y=None) == q.QGEMM_OK
+        assert f(N=0, X=None, W=None, S=None, Y=None) == q.QGEMM_OK
+    monkeypatch.setenv("QGEMM_FAKE_ARCH", "gfx1201")
+    assert i4() == q.QGEMM_ERR_UNSUPPORTED_DEVICE and mx() == q.QGEMM_ERR_UNSUPPORTED_DEVICE
+    monkeypatch.setenv("QGEMM_FAKE_ARCH", "gfx950")
+    monkeypatch.setenv("QGEMM_INJECT_LAUNCH_ERROR", "719")
+    assert i4() == q.QGEMM_ERR_HIP and mx() == q.QGEMM_ERR_HIP
