@@ -722,6 +722,16 @@ def qgemm_mx_prepacked(fmt, A, Bp, scale_a, scale_b, b_layout, bias=None, out=No
     return out
 
 
-from .layer import (KV8Cache, qgemm_kv8_append, qgemm_kv8_attention, qgemm_rmsnorm_quant_f8_block,  # noqa: E402,F401
-                    qgemm_rmsnorm_quant_f8_pertoken, qgemm_rmsnorm_quant_i8_rowwise, qgemm_rmsnorm_quant_mx,
-                    qgemm_w4_matvec_i4, qgemm_w4_matvec_mx)
+# The decoder-layer operators live in layer.py, which needs torch at import;
+# they are looked up on first use, so that the package itself does not.
+_LAYER = ("KV8Cache", "qgemm_kv8_append", "qgemm_kv8_attention", "qgemm_rmsnorm_quant_f8_block",
+          "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_mx",
+          "qgemm_w4_matvec_i4", "qgemm_w4_matvec_mx")
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layer
+    globals().update({n: getattr(layer, n) for n in _LAYER})
+    return globals()[name]

@@ -301,6 +301,7 @@ qgemm_status qgemm_w4_matvec_i4(const uint16_t *X, int64_t ldx, const uint8_t *W
     a.ldw = ldw;
     a.ldy = ldy;
     a.group = (int)group;
+    a.srows = 1;
     return w4_common(a, M, N, K, group, stream);
 }
 

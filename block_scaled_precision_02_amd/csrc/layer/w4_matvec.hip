@@ -43,11 +43,20 @@ __device__ __forceinline__ u32x4 swap4(u32x4 w)
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight nibbles as 128 + w, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 nibbles_bf16(unsigned w)
+// Eight nibbles as 128 + w, in the order 0 4 1 5 2 6 3 7; base: 128 twice, in
+// a vector register (an instruction takes one scalar operand, so that with two
+// constants the and-or would be two).
+__device__ __forceinline__ unsigned nibble_base()
 {
-    constexpr unsigned M = 0x000f000fu, B = 0x43004300u;
-    return __builtin_bit_cast(bf16x8, u32x4{(w & M) | B, ((w >> 4) & M) | B, ((w >> 8) & M) | B, ((w >> 12) & M) | B});
+    unsigned b = 0x43004300u;
+    asm("" : "+v"(b));
+    return b;
+}
+__device__ __forceinline__ bf16x8 nibbles_bf16(unsigned w, unsigned base)
+{
+    constexpr unsigned M = 0x000f000fu;
+    return __builtin_bit_cast(
+        bf16x8, u32x4{(w & M) | base, ((w >> 4) & M) | base, ((w >> 8) & M) | base, ((w >> 12) & M) | base});
 }
 
 // Eight e2m1 codes times scale (a power of two).
@@ -69,6 +78,25 @@ __device__ __forceinline__ bf16x8 x_order(u32x4 x)
                                             __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)});
 }
 
+// The x of a chunk as product operands, from four loads of which number p holds
+// elements 32 p + 8 g .. + 7 (the four lane groups side by side: 64 bytes of a
+// row an instruction; a lane's own 32 elements would be 64 separate pieces).
+// Where the weights are not exchanged between the lane groups, x is: product p
+// then takes elements 32 g + 8 p of lane group g.
+template <bool SWAP>
+__device__ __forceinline__ void x_operands(u32x4 (&v)[4])
+{
+    if constexpr (!SWAP) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x4 t = swap4(u32x4{v[0][i], v[1][i], v[2][i], v[3][i]});
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                v[p][i] = t[p];
+        }
+    }
+}
+
 // GROUP 0: mx; else i4 with that group.  MT 16-row tiles of x, of which RI of
 // every 4 accumulators hold rows (row t of a tile stands in product row
 // 4 (t % 4) + t / 4, so that 4 RI rows need RI of them).  NT 16-row tiles of
@@ -80,7 +108,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
     constexpr bool SWAP = GROUP == 32 || GROUP == 64;
     constexpr int SC = MX ? 1 : CHUNK / GROUP;   // scales of a chunk
     constexpr int U = 4 / NT;                    // chunks loaded ahead together
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * (16 * NT);
     const int chunks = (a.K + CHUNK - 1) / CHUNK, groups = a.K / (MX ? 32 : GROUP);
@@ -102,7 +130,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
     for (int t = 0; t < MT; ++t) {
         const int row = 16 * t + (r16 >> 2) + 4 * (r16 & 3);
         has[t] = row < a.M;
-        x[t] = a.X + (int64_t)(has[t] ? row : 0) * a.ldx + (SWAP ? 8 : 32) * g;
+        x[t] = a.X + (int64_t)(has[t] ? row : 0) * a.ldx + 8 * g;
     }
 
     f32x4 acc[MT][NT];
@@ -113,6 +141,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
             acc[i][t] = f32x4{0, 0, 0, 0};
     const u32x4 one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+    [[maybe_unused]] const unsigned base = nibble_base();
 
     for (int cb = c0; cb < c1; cb += U) {
         u32x4 wv[U][NT];
@@ -125,7 +154,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
             const int64_t off = min((int64_t)c * (CHUNK / 2), (int64_t)(a.K / 2) - 16 * g - 16);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                wv[u][t] = __builtin_nontemporal_load((const u32x4 *)(w[t] + off));
+                wv[u][t] = *(const u32x4 *)(w[t] + off);
                 if constexpr (MX) {
                     sv[u][t][0] = sb[t][min(4 * c + g, groups - 1)];
                 } else {
@@ -145,13 +174,18 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
                 break;
             u32x4 xv[MT][4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const int k = c * CHUNK + (SWAP ? 32 * p : 8 * p);
-                    const bool in = has[i] && (SWAP ? k < a.K : c * CHUNK + 32 * g < a.K);
-                    xv[i][p] = in ? *(const u32x4 *)(x[i] + k) : u32x4{0, 0, 0, 0};
+                    const int k = c * CHUNK + 32 * p;
+                    const bool in = has[i] && k < a.K;
+                    xv[i][p] = *(const u32x4 *)(in ? x[i] + k : a.X);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        xv[i][p][e] = in ? xv[i][p][e] : 0u;
                 }
+                x_operands<SWAP>(xv[i]);
+            }
             if constexpr (MX) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -174,7 +208,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
                     const u32x4 v = SWAP ? swap4(wv[u][t]) : wv[u][t];
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        wf[t][p] = nibbles_bf16(v[p]);
+                        wf[t][p] = nibbles_bf16(v[p], base);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -231,25 +265,308 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
         }
 }
 
-template <int GROUP, int MT, int RI>
-hipError_t launch_nt(const W4Args &a, hipStream_t s)
+// The same for up to 16 rows and K up to 8192, the ordinary decode step: a
+// workgroup stays and walks over 16-row tiles of weights.  Wave v's chunks are
+// the same for every tile, so that x (XR rows of it) is laid out once in LDS in
+// the order of the products' operands, and so are its sums over the groups; a
+// product's rows without a row of x repeat others, as nobody reads their sums.
+// Up to four rows that leaves room for two workgroups a CU.  Where x is too
+// long for LDS, K goes in parts, one walk each, with the tiles' sums kept in
+// LDS between them.  A chunk's register takes the next tile's weights as soon
+// as it is used.  A tile's scales lie side by side in memory: the workgroup
+// fetches them 16 bytes a thread, a tile ahead, and takes them from LDS (a byte
+// or two at a time from memory took 6 of 19 us at 1x8192x8192).
+// CPW: chunks a wave and part, at most.
+template <int GROUP, int XR, int CPW, bool ZERO>
+__global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel(W4Args a)
 {
-    constexpr int NT = 1;
-    const unsigned grid = (unsigned)((a.N + 16 * NT - 1) / (16 * NT));
-    hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, NT>), dim3(grid), dim3(W4_WAVES * 64), 0, s, a);
+    constexpr int W = W4_WAVES;
+    constexpr bool MX = GROUP == 0;
+    constexpr bool SWAP = GROUP == 32 || GROUP == 64;
+    constexpr int RI = XR == 16 ? 4 : XR == 8 ? 2 : 1;   // accumulators that hold rows of x
+    constexpr int SC = MX ? 4 : CHUNK / GROUP;           // scales of a chunk
+    constexpr int PG = 4 / SC;                           // products of a scale
+    constexpr int ESZ = MX ? 1 : 2;                      // bytes of a scale
+    // a tile's scales and zero points: rows of K <= 8192, 16 bytes further apart
+    // where they are whole 16-byte pieces (rows 256 bytes apart are one bank)
+    constexpr int KC = XR >= 8 ? 64 : W * CPW;           // chunks of a row, at most
+    constexpr int SB = 16 * (KC * SC * ESZ + 16), ZB = ZERO ? 16 * (KC * SC + 16) : 0;
+    constexpr int NX = (CPW * XR + 3) / 4;               // 16-byte pieces of x a thread lays out
+    extern __shared__ u32x4 xl[];                        // [chunk][product][lane group][XR], then the tiles' sums
+    __shared__ float red[2][W][16][17];
+    __shared__ alignas(16) uint8_t tab[2][SB + ZB];
+    __shared__ alignas(16) float xsum[MX ? 1 : W * CPW][4][SC][RI];   // sums of x, [chunk][lane group]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int chunks = (a.K + CHUNK - 1) / CHUNK, groups = a.K / (MX ? 32 : GROUP);
+    const int parts = (chunks + W * CPW - 1) / (W * CPW);
+    const int tiles = (a.N + 15) / 16, step = gridDim.x;
+    const int pr = threadIdx.x >> 4, col = threadIdx.x & 15, xr = (pr >> 2) + 4 * (pr & 3);   // a result's place
+    float *const kept = (float *)(xl + W * CPW * 16 * XR) + threadIdx.x;                      // 256 a tile
+
+    // bytes of a row's scales, of a tile's (a 32-row scale: one row, for two
+    // tiles), of the whole arrays; the pitch and this thread's place in LDS
+    const int srows = MX ? a.srows : 1, row_b = groups * ESZ, lim = (srows == 1 ? 16 : 1) * row_b;
+    const int at_t = 16 * threadIdx.x;
+    const int s_pitch = row_b + (row_b % 16 ? 0 : 16), z_pitch = groups + (groups % 16 ? 0 : 16);
+    const int s_to = row_b % 16 ? at_t : at_t + 16 * (at_t / row_b);
+    [[maybe_unused]] const int z_to = SB + (groups % 16 ? at_t : at_t + 16 * (at_t / groups));
+    const int64_t s_all = (int64_t)((a.N + srows - 1) / srows) * row_b;
+    const auto start = [&](int tile) { return (int64_t)(tile * 16 / srows) * row_b; };
+    u32x4 wv[CPW], sv, zv;   // the weights, and this thread's 16 bytes of scales and zero points
+    const auto load_scales = [&](int tile) {
+        const int64_t at = start(tile) + at_t;
+        sv = *(const u32x4 *)((const uint8_t *)a.S + (at_t < lim && at + 16 <= s_all ? at : 0));
+        if constexpr (ZERO) {
+            const int64_t az = start(tile) / 2 + at_t;
+            zv = *(const u32x4 *)(a.Z + (at_t < lim / 2 && az + 16 <= s_all / 2 ? az : 0));
+        }
+    };
+    // the scales to LDS; what lies past the arrays' last whole 16 bytes comes
+    // byte by byte
+    const auto stage = [&](int tile, uint8_t *to) {
+        const int64_t at = start(tile) + at_t;
+        if (at_t < lim) {
+            if (at + 16 <= s_all)
+                *(u32x4 *)(to + s_to) = sv;
+            else
+                for (int i = 0; i < 16 && at + i < s_all; ++i)
+                    to[s_to + i] = ((const uint8_t *)a.S)[at + i];
+        }
+        if constexpr (ZERO) {
+            const int64_t az = start(tile) / 2 + at_t;
+            if (at_t < lim / 2) {
+                if (az + 16 <= s_all / 2)
+                    *(u32x4 *)(to + z_to) = zv;
+                else
+                    for (int i = 0; i < 16 && az + i < s_all / 2; ++i)
+                        to[z_to + i] = a.Z[az + i];
+            }
+        }
+    };
+    const auto weights = [&](int tile) { return a.W + (int64_t)min(tile * 16 + r16, a.N - 1) * a.ldw + 16 * g; };
+    [[maybe_unused]] const unsigned base = nibble_base();
+    // the row of x that stands in a product's row
+    const int xslot = XR == 1 ? 0 : XR == 4 ? r16 >> 2 : XR == 8 ? (r16 >> 2) + 4 * (r16 & 1) : (r16 >> 2) + 4 * (r16 & 3);
+
+    for (int part = 0; part < parts; ++part) {
+        const int p0 = chunks * part / parts, pn = chunks * (part + 1) / parts - p0;   // W <= pn <= W * CPW
+        const int l0 = pn * wave / W, c0 = p0 + l0, nc = pn * (wave + 1) / W - l0;     // 1 <= nc <= CPW
+        // every wave loads CPW chunks, its last one again past its own count;
+        // weights past K (a last chunk of 32, 64 or 96) are any that are there,
+        // as x is zero for them
+        const auto load_chunk = [&](const uint8_t *w, int c) {
+            const int off = min((c0 + min(c, nc - 1)) * (CHUNK / 2), a.K / 2 - 16 * g - 16);
+            return *(const u32x4 *)(w + off);
+        };
+        const auto operand = [&](int c, int p) {
+            return __builtin_bit_cast(bf16x8, xl[(((l0 + c) * 4 + p) * 4 + g) * XR + xslot]);
+        };
+        if (part)
+            __syncthreads();   // x and the tables of the part before are done with
+        // x first: what is loaded first is there first
+        u32x4 xp[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int at = threadIdx.x + i * (W * 64);
+            const int row = at % XR, pg = at / XR % 16, c = p0 + at / XR / 16;
+            const int k = c * CHUNK + (SWAP ? 8 * pg : 32 * (pg & 3) + 8 * (pg >> 2));
+            const bool in = row < a.M && k < a.K;
+            xp[i] = *(const u32x4 *)(in ? a.X + (int64_t)row * a.ldx + k : a.X);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                xp[i][e] = in ? xp[i][e] : 0u;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_scales(blockIdx.x);
+        {
+            const uint8_t *w = weights(blockIdx.x);
+#pragma unroll
+            for (int c = 0; c < CPW; ++c)
+                wv[c] = load_chunk(w, c);
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int at = threadIdx.x + i * (W * 64);
+            if (at < pn * 16 * XR)
+                xl[at] = MX ? xp[i] : __builtin_bit_cast(u32x4, x_order(xp[i]));
+        }
+        stage(blockIdx.x, tab[0]);
+        __syncthreads();
+        if constexpr (!MX) {
+            // sums of x over the groups: products with ones, whose columns are all alike
+            const u32x4 one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+            const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+            for (int c = 0; c < nc; ++c)
+#pragma unroll
+                for (int j = 0; j < SC; ++j) {
+                    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+                    for (int p = j * PG; p < (j + 1) * PG; ++p)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(c, p), ones, sum, 0, 0, 0);
+                    if (r16 == 0)
+#pragma unroll
+                        for (int r = 0; r < RI; ++r)
+                            xsum[l0 + c][g][j][r] = sum[r];   // read by this wave alone
+                }
+        }
+
+        // A tile: its sums, with the next one's loads; the next one's scales to
+        // LDS; one barrier (a buffer's last readers have passed the barrier of
+        // the tile between); the result.
+        int flip = 0, nth = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += step, flip ^= 1, ++nth) {
+            const int next = min(tile + step, tiles - 1);
+            const uint8_t *w = weights(next), *sz = tab[flip];
+            load_scales(next);
+            // x and its sums are the same for every tile: an offset that the
+            // compiler cannot see through keeps them in LDS and out of the registers
+            int here = 0;
+            asm volatile("" : "+s"(here));
+            f32x4 acc = {0, 0, 0, 0};
+            const int row = min(r16, a.N - 1 - tile * 16);
+            const uint8_t *srow = sz + (srows == 1 ? row * s_pitch : 0);
+            [[maybe_unused]] const uint8_t *zrow = sz + SB + row * z_pitch;
+#pragma unroll
+            for (int c = 0; c < CPW; ++c) {
+                if (c >= nc)
+                    break;
+                const u32x4 wc = wv[c];
+                wv[c] = load_chunk(w, c);
+                const int at = (c0 + c) * SC;
+                if constexpr (MX) {
+                    // a group past K (x is zero there) takes any scale of the row
+                    const unsigned s = srow[min(at + g, groups - 1)];
+                    const float scale = __uint_as_float(s == 255u ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(c + here, p), e2m1_bf16(wc[p], scale), acc, 0,
+                                                                      0, 0);
+                } else {
+                    const u32x4 v = SWAP ? swap4(wc) : wc;
+                    struct alignas(2 * SC) Scales {
+                        uint16_t s[SC];
+                    };
+                    struct alignas(SC) Zeros {
+                        uint8_t z[SC];
+                    };
+                    const Scales s4 = *(const Scales *)(srow + 2 * at);
+                    [[maybe_unused]] Zeros z4;
+                    if constexpr (ZERO)
+                        z4 = *(const Zeros *)(zrow + at);
+#pragma unroll
+                    for (int j = 0; j < SC; ++j) {
+                        f32x4 part_sum = {0, 0, 0, 0};
+#pragma unroll
+                        for (int p = j * PG; p < (j + 1) * PG; ++p)
+                            part_sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(c + here, p),
+                                                                               nibbles_bf16(v[p], base), part_sum, 0, 0, 0);
+                        const float s = __uint_as_float((unsigned)s4.s[j] << 16);
+                        const float z = ZERO ? 128.0f + (float)z4.z[j] : 136.0f;
+#pragma unroll
+                        for (int r = 0; r < RI; ++r)
+                            acc[r] = fmaf(fmaf(-z, xsum[l0 + c + here][g][j][r], part_sum[r]), s, acc[r]);
+                    }
+                }
+            }
+            stage(next, tab[flip ^ 1]);
+#pragma unroll
+            for (int r = 0; r < RI; ++r)
+                red[flip][wave][4 * g + r][r16] = acc[r];
+            __syncthreads();
+            const int n = tile * 16 + col;
+            if (pr < 16 && xr < a.M && n < a.N) {
+                float y = 0.0f;
+#pragma unroll
+                for (int v = 0; v < W; ++v)
+                    y += red[flip][v][pr][col];
+                if (part)
+                    y += kept[256 * nth];   // this thread's own
+                if (part + 1 < parts) {
+                    kept[256 * nth] = y;
+                } else {
+                    if (a.bias)
+                        y += lo_bf16(a.bias[n]);
+                    a.Y[(int64_t)xr * a.ldy + n] = (uint16_t)pack_bf16(y, 0.0f);
+                }
+            }
+        }
+    }
+}
+
+template <int GROUP, int MT, int RI>
+hipError_t launch_wide(const W4Args &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, 1>), dim3((unsigned)((a.N + 15) / 16)), dim3(W4_WAVES * 64), 0,
+                       s, a);
     return hipGetLastError();
+}
+
+template <int GROUP, int XR, int CPW>
+hipError_t launch_cpw(const W4Args &a, hipStream_t s)
+{
+    constexpr int NUM_CU = 256, KEPT = 8;   // tiles whose sums are kept, at most
+    const int tiles = (a.N + 15) / 16, chunks = (a.K + CHUNK - 1) / CHUNK;
+    int wgs = XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
+    if (chunks > W4_WAVES * CPW) {
+        wgs = wgs > (tiles + KEPT - 1) / KEPT ? wgs : (tiles + KEPT - 1) / KEPT;
+        kept = (tiles + wgs - 1) / wgs;
+    }
+    const dim3 grid((unsigned)(tiles < wgs ? tiles : wgs)), block(W4_WAVES * 64);
+    const size_t lds = (size_t)W4_WAVES * CPW * 16 * XR * 16 + kept * 1024;
+    if constexpr (GROUP != 0) {
+        if (a.Z) {
+            hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, true>), grid, block, lds, s, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, false>), grid, block, lds, s, a);
+    return hipGetLastError();
+}
+
+template <int GROUP, int XR>
+hipError_t launch_walk(const W4Args &a, hipStream_t s)
+{
+    // 64 KB of x a part, or 128 where the scales leave room; longer K in parts
+    constexpr int MOST = XR == 16 ? (GROUP == 0 ? 4 : 3) : XR == 8 ? 4 : 8;
+    const int cpw = ((a.K + CHUNK - 1) / CHUNK + W4_WAVES - 1) / W4_WAVES;
+    if (cpw <= 1)
+        return launch_cpw<GROUP, XR, 1>(a, s);
+    if (cpw <= 2)
+        return launch_cpw<GROUP, XR, 2>(a, s);
+    if constexpr (MOST == 8) {
+        if (cpw <= 4)
+            return launch_cpw<GROUP, XR, 4>(a, s);
+        if (cpw <= 6)
+            return launch_cpw<GROUP, XR, 6>(a, s);
+    }
+    return launch_cpw<GROUP, XR, MOST>(a, s);
 }
 
 template <int GROUP>
 hipError_t launch_rows(const W4Args &a, hipStream_t s)
 {
+    const int chunks = (a.K + CHUNK - 1) / CHUNK;
+    const int64_t groups = a.K / (GROUP ? GROUP : 32);
+    // the walk has a chunk for every wave, eight at most, and reads scales 16
+    // bytes at a time; int4's groups a chunk at a time
+    const bool walk = a.M <= 16 && (GROUP == 0 || a.K % CHUNK == 0) && chunks >= W4_WAVES && chunks <= 8 * W4_WAVES && (uintptr_t)a.S % 16 == 0 &&
+                      (uintptr_t)a.Z % 16 == 0 && (a.srows == 1 || groups % 16 == 0) &&
+                      a.N * groups >= 16 * a.srows;
+    if (walk) {
+        if (a.M == 1)
+            return launch_walk<GROUP, 1>(a, s);
+        if (a.M <= 4)
+            return launch_walk<GROUP, 4>(a, s);
+        return a.M <= 8 ? launch_walk<GROUP, 8>(a, s) : launch_walk<GROUP, 16>(a, s);
+    }
     if (a.M <= 4)
-        return launch_nt<GROUP, 1, 1>(a, s);
+        return launch_wide<GROUP, 1, 1>(a, s);
     if (a.M <= 16)
-        return launch_nt<GROUP, 1, 4>(a, s);
+        return launch_wide<GROUP, 1, 4>(a, s);
     if (a.M <= 32)
-        return launch_nt<GROUP, 2, 4>(a, s);
-    return launch_nt<GROUP, 4, 4>(a, s);
+        return launch_wide<GROUP, 2, 4>(a, s);
+    return launch_wide<GROUP, 4, 4>(a, s);
 }
 
 }  // namespace

@@ -5,53 +5,101 @@ import ctypes
 
 import torch
 
-from . import (QGEMM_KV8_E4M3, QGEMM_KV8_I8, QGEMM_MX_E2M1, QGEMM_MX_E4M3, _check, _codes_out, _ld_bytes, _operand, _ptr, _same_device, _stream,
-               _vector, lib)
+from . import (QGEMM_KV8_E4M3, QGEMM_KV8_I8, QGEMM_MX_E2M1, QGEMM_MX_E4M3, _check, _codes_out, lib)
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_empty = torch.empty
+
+# These calls stand between the GEMMs of a decode step, where the host's time is
+# the step's: attributes are read once, and the device is changed only where it
+# is not the current one.
+
+
+def _enqueue(entry, device, stream, *args):
+    """entry(*args, stream) on device; raises what it reports."""
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = entry(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, stream)
+    if status:
+        _check(status)
+
+
+def _rows(t, name, dtypes=_BF16):
+    """Shape and row stride (elements) of a 2-D GPU tensor with unit stride
+    along its rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor of {dtypes}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return shape, strides[0] if shape[0] > 1 else shape[1]
+
+
+def _vec(t, name, n, device, dtypes=_BF16):
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device or t.numel() != n \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtypes} with {n} elements on {device}")
+    return t.data_ptr()
 
 
 # ------------------------------------------------------------ RMS norm
 
-def _bf16_rows(t, name, shape, device):
-    if t is None:
-        return 0
-    ld = _operand(t, name, _BF16) // 2
-    if tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}] on {device}, got {tuple(t.shape)} on {t.device}")
-    return ld
+def _norm_common(X, gamma, residual, residual_out):
+    """What the four norms share: (shape, device, the arguments up to gamma,
+    residual_out, its pointer and stride)."""
+    shape, ldx = _rows(X, "X")
+    device = X.device
+    pr = ldr = po = ldo = 0
+    if residual is not None:
+        rshape, ldr = _rows(residual, "residual")
+        if rshape != shape or residual.device != device:
+            raise ValueError(f"residual must be {tuple(shape)} on {device}, got {tuple(rshape)} on {residual.device}")
+        pr = residual.data_ptr()
+        if residual_out is None:
+            residual_out = _empty(shape, dtype=torch.bfloat16, device=device)
+    if residual_out is not None:
+        oshape, ldo = _rows(residual_out, "residual_out")
+        if oshape != shape or residual_out.device != device:
+            raise ValueError(f"residual_out must be {tuple(shape)} on {device}, got {tuple(oshape)} on "
+                             f"{residual_out.device}")
+        po = residual_out.data_ptr()
+    return (shape, device, (X.data_ptr(), ldx, pr or None, ldr, _vec(gamma, "gamma", shape[1], device)),
+            residual_out, po or None, ldo)
 
 
-def _norm_args(X, gamma, residual, residual_out):
-    """The tensors and strides common to the four norms."""
-    ldx = _operand(X, "X", _BF16) // 2
-    shape, device = tuple(X.shape), X.device
-    ldr = _bf16_rows(residual, "residual", shape, device)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    ldo = _bf16_rows(residual_out, "residual_out", shape, device)
-    _vector(gamma, "gamma", shape[1], _BF16)
-    _same_device(device, gamma)
-    return ldx, ldr, ldo, residual_out
-
-
-def _norm_row(entry, code_dtype, X, gamma, eps, residual, residual_out, out, scale, stream):
-    ldx, ldr, ldo, residual_out = _norm_args(X, gamma, residual, residual_out)
-    M, K = X.shape
-    if code_dtype is torch.int8:
-        if out is None:
-            out = torch.empty((M, K + (-K) % 16), dtype=torch.int8, device=X.device)[:, :K]
-        elif tuple(out.shape) != (M, K) or out.dtype != torch.int8 or (K > 1 and out.stride(1) != 1):
-            raise ValueError(f"out must be int8 [{M}, {K}] with unit stride along K")
+def _norm_codes(out, M, row, device, dtype):
+    """The codes' tensor and row stride in bytes."""
+    if out is None:
+        wide = row + (-row) % 16          # the library's rule for row strides
+        out = _empty((M, wide), dtype=dtype, device=device)
+        return (out if wide == row else out[:, :row]), wide
+    if dtype is torch.int8:
+        if tuple(out.shape) != (M, row) or out.dtype != torch.int8 or out.device != device or (
+                row > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be int8 [{M}, {row}] with unit stride along K on {device}")
     else:
-        out = _codes_out(out, (M, K), X.device, "out")
+        out = _codes_out(out, (M, row), device, "out")
+    return out, out.stride(0) if M > 1 else row + (-row) % 16
+
+
+def _norm_row(entry, dtype, X, gamma, eps, residual, residual_out, out, scale, stream):
+    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out)
+    out, ldq = _norm_codes(out, M, K, device, dtype)
     if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=X.device)
-    _vector(scale, "scale", M, (torch.float32,))
-    _same_device(X.device, out, scale)
-    with torch.cuda.device(X.device):
-        _check(entry(_ptr(X), ldx, _ptr(residual), ldr, _ptr(gamma), eps, _ptr(residual_out), ldo, _ptr(out),
-                     _ld_bytes(out, K), _ptr(scale), M, K, _stream(X.device, stream)))
+        scale = _empty(M, dtype=torch.float32, device=device)
+        ps = scale.data_ptr()
+    else:
+        ps = _vec(scale, "scale", M, device, (torch.float32,))
+    _enqueue(entry, device, stream, *head, eps, po, ldo, out.data_ptr(), ldq, ps, M, K)
     return out, scale, residual_out
 
 
@@ -73,13 +121,17 @@ def qgemm_rmsnorm_quant_f8_pertoken(X, gamma, eps=1e-6, residual=None, residual_
                      scale, stream)
 
 
-def _norm_scales(scales, shape, dtype, device):
-    if scales is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if (scales.dtype != dtype or tuple(scales.shape) != shape or scales.device != device
-            or (shape[1] > 1 and scales.stride(1) != 1)):
-        raise ValueError(f"scale must be {dtype} {shape} with unit stride along its rows on {device}")
-    return scales
+def _norm_block(entry, first, row, parts, dtype, X, gamma, eps, residual, residual_out, out, scale, stream):
+    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out)
+    out, ldq = _norm_codes(out, M, row, device, torch.uint8)
+    if scale is None:
+        scale, lds = _empty((M, parts), dtype=dtype, device=device), parts
+    else:
+        sshape, lds = _rows(scale, "scale", (dtype,))
+        if tuple(sshape) != (M, parts) or scale.device != device:
+            raise ValueError(f"scale must be {dtype} [{M}, {parts}] on {device}")
+    _enqueue(entry, device, stream, *first, *head, eps, po, ldo, out.data_ptr(), ldq, scale.data_ptr(), lds, M, K)
+    return out, scale, residual_out
 
 
 def qgemm_rmsnorm_quant_f8_block(X, gamma, eps=1e-6, residual=None, residual_out=None, out=None, scale=None,
@@ -87,18 +139,11 @@ def qgemm_rmsnorm_quant_f8_block(X, gamma, eps=1e-6, residual=None, residual_out
     """RMS norm of X + residual -> (e4m3 codes as uint8 [M, K], scales fp32
     [M, K/128], the sum in bf16): the A operand and scale_a of
     qgemm_f8_blockscale.  K a multiple of 128."""
-    ldx, ldr, ldo, residual_out = _norm_args(X, gamma, residual, residual_out)
-    M, K = X.shape
+    K = X.shape[-1]
     if K % 128:
         raise ValueError(f"K={K} is not a multiple of 128")
-    out = _codes_out(out, (M, K), X.device, "out")
-    scale = _norm_scales(scale, (M, K // 128), torch.float32, X.device)
-    lds = scale.stride(0) if M > 1 else K // 128
-    with torch.cuda.device(X.device):
-        _check(lib().qgemm_rmsnorm_quant_f8_block(_ptr(X), ldx, _ptr(residual), ldr, _ptr(gamma), eps,
-                                                  _ptr(residual_out), ldo, _ptr(out), _ld_bytes(out, K), _ptr(scale),
-                                                  lds, M, K, _stream(X.device, stream)))
-    return out, scale, residual_out
+    return _norm_block(lib().qgemm_rmsnorm_quant_f8_block, (), K, K // 128, torch.float32, X, gamma, eps, residual,
+                       residual_out, out, scale, stream)
 
 
 def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=None, out=None, scale=None,
@@ -108,17 +153,9 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
     scale_a of qgemm_mx."""
     if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
         raise ValueError(f"unknown MX format {fmt}")
-    ldx, ldr, ldo, residual_out = _norm_args(X, gamma, residual, residual_out)
-    M, K = X.shape
-    row = K if fmt == QGEMM_MX_E4M3 else K // 2
-    out = _codes_out(out, (M, row), X.device, "out")
-    scale = _norm_scales(scale, (M, K // 32), torch.uint8, X.device)
-    lds = scale.stride(0) if M > 1 else K // 32
-    with torch.cuda.device(X.device):
-        _check(lib().qgemm_rmsnorm_quant_mx(fmt, _ptr(X), ldx, _ptr(residual), ldr, _ptr(gamma), eps,
-                                            _ptr(residual_out), ldo, _ptr(out), _ld_bytes(out, row), _ptr(scale), lds,
-                                            M, K, _stream(X.device, stream)))
-    return out, scale, residual_out
+    K = X.shape[-1]
+    return _norm_block(lib().qgemm_rmsnorm_quant_mx, (fmt,), K if fmt == QGEMM_MX_E4M3 else K // 2, K // 32,
+                       torch.uint8, X, gamma, eps, residual, residual_out, out, scale, stream)
 
 
 # ------------------------------------------------------------ 8-bit cache
@@ -175,32 +212,34 @@ class KV8Cache:
                    torch.empty((num_blocks, kv_heads), dtype=torch.float32, device=device))
 
 
-def _token_rows(t, name, heads, dim, device):
-    """Token stride (elements) of a [tokens, heads, dim] bf16 tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _BF16 or t.device != device:
-        raise ValueError(f"{name} must be a bfloat16 tensor on {device}")
+def _token_rows(t, name, heads, dim, device, dtypes=_BF16):
+    """Shape and token stride (elements) of a [tokens, heads, dim] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{name} must be a tensor of {dtypes} on {device}")
     shape, st = t.shape, t.stride()
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(shape)}")
     if st[2] != 1 or (shape[1] > 1 and st[1] != dim):
         raise ValueError(f"{name} must have unit stride along its last axis and adjacent heads")
-    return st[0] if shape[0] > 1 else shape[1] * dim
+    return shape, st[0] if shape[0] > 1 else shape[1] * dim
 
 
 def _sequences(table, cu, lens, device):
-    batch = lens.shape[0]
-    for name, t in (("block_table", table), ("cu_seqlens", cu), ("kv_lens", lens)):
-        if t.dtype != torch.int32 or t.device != device:
-            raise ValueError(f"{name} must be int32 on {device}, got {t.dtype} on {t.device}")
-    if lens.dim() != 1 or cu.dim() != 1 or cu.shape[0] != batch + 1 or not lens.is_contiguous() \
+    """(table pointer, stride, width), cu pointer, lens pointer, batch."""
+    i32 = torch.int32
+    if table.dtype != i32 or cu.dtype != i32 or lens.dtype != i32 or table.device != device or cu.device != device \
+            or lens.device != device:
+        raise ValueError(f"block_table, cu_seqlens and kv_lens must be int32 on {device}")
+    batch, tshape, tstride = lens.numel(), table.shape, table.stride()
+    if lens.dim() != 1 or cu.dim() != 1 or cu.numel() != batch + 1 or not lens.is_contiguous() \
             or not cu.is_contiguous():
         raise ValueError(f"kv_lens must be [batch] and cu_seqlens [batch + 1], contiguous; got {tuple(lens.shape)} and "
                          f"{tuple(cu.shape)}")
-    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"block_table must be [{batch}, blocks] with unit stride along its rows, got "
-                         f"{tuple(table.shape)}")
-    width = table.shape[1]
-    return batch, max(table.stride(0), width) if batch > 1 else width, width
+    if len(tshape) != 2 or tshape[0] != batch or (tshape[1] > 1 and tstride[1] != 1):
+        raise ValueError(f"block_table must be [{batch}, blocks] with unit stride along its rows, got {tuple(tshape)}")
+    width = tshape[1]
+    ldt = tstride[0] if batch > 1 and tstride[0] > width else width
+    return table.data_ptr(), ldt, width, cu.data_ptr(), lens.data_ptr(), batch
 
 
 def qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q, stream=None):
@@ -211,15 +250,13 @@ def qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q, strea
     [batch] the lengths with them; max_q at least the most new tokens of a
     sequence."""
     device = cache.device
-    ldk = _token_rows(K, "K", cache.kv_heads, cache.head_dim, device)
-    ldv = _token_rows(V, "V", cache.kv_heads, cache.head_dim, device)
-    tokens = K.shape[0]
-    if V.shape[0] != tokens:
-        raise ValueError(f"K holds {tokens} tokens, V {V.shape[0]}")
-    batch, ldt, width = _sequences(block_table, cu_seqlens, kv_lens, device)
-    with torch.cuda.device(device):
-        _check(lib().qgemm_kv8_append(cache._ref, _ptr(K), ldk, _ptr(V), ldv, _ptr(block_table), ldt, width,
-                                      _ptr(cu_seqlens), _ptr(kv_lens), tokens, batch, max_q, _stream(device, stream)))
+    kshape, ldk = _token_rows(K, "K", cache.kv_heads, cache.head_dim, device)
+    vshape, ldv = _token_rows(V, "V", cache.kv_heads, cache.head_dim, device)
+    if vshape != kshape:
+        raise ValueError(f"K holds {kshape[0]} tokens, V {vshape[0]}")
+    pt, ldt, width, pc, pl, batch = _sequences(block_table, cu_seqlens, kv_lens, device)
+    _enqueue(lib().qgemm_kv8_append, device, stream, cache._ref, K.data_ptr(), ldk, V.data_ptr(), ldv, pt, ldt, width,
+             pc, pl, kshape[0], batch, max_q)
 
 
 def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_kv, sm_scale=None, causal=True,
@@ -232,82 +269,85 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
     at least qgemm_kv8_attention_workspace(...) bytes, allocated here if not
     given.  Tokens of no sequence are left as they are in ``out``."""
     device = cache.device
-    ldq = _token_rows(Q, "Q", None, cache.head_dim, device)
-    tokens, heads = Q.shape[0], Q.shape[1]
-    batch, ldt, width = _sequences(block_table, cu_seqlens, kv_lens, device)
+    shape, ldq = _token_rows(Q, "Q", None, cache.head_dim, device)
+    tokens, heads, dim = shape
+    pt, ldt, width, pc, pl, batch = _sequences(block_table, cu_seqlens, kv_lens, device)
     if out is None:
-        out = torch.empty((tokens, heads, cache.head_dim), dtype=torch.bfloat16, device=device)
-    elif out.dtype != torch.bfloat16 or out.shape[0] != tokens:
-        raise ValueError(f"out must be bfloat16 [{tokens}, {heads}, {cache.head_dim}]")
-    ldo = _token_rows(out, "out", heads, cache.head_dim, device)
+        out, ldo = _empty(shape, dtype=torch.bfloat16, device=device), heads * dim
+    else:
+        oshape, ldo = _token_rows(out, "out", heads, dim, device, (torch.bfloat16,))
+        if oshape != shape:
+            raise ValueError(f"out must be bfloat16 {tuple(shape)}")
     if sm_scale is None:
-        sm_scale = cache.head_dim ** -0.5
+        sm_scale = dim ** -0.5
     causal = 1 if causal else 0
+    L = lib()
+    pw = nbytes = 0
     if workspace is None:
-        need = lib().qgemm_kv8_attention_workspace(cache._ref, tokens, batch, heads, max_q, max_kv, causal, window)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        nbytes = L.qgemm_kv8_attention_workspace(cache._ref, tokens, batch, heads, max_q, max_kv, causal, window)
+        if nbytes > 0:
+            workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+            pw = workspace.data_ptr()
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(device):
-        _check(lib().qgemm_kv8_attention(cache._ref, _ptr(Q), ldq, _ptr(block_table), ldt, width, _ptr(cu_seqlens),
-                                         _ptr(kv_lens), tokens, batch, heads, max_q, max_kv, sm_scale, causal, window,
-                                         _ptr(out), ldo, _ptr(workspace), nbytes, _stream(device, stream)))
+    else:
+        pw, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _enqueue(L.qgemm_kv8_attention, device, stream, cache._ref, Q.data_ptr(), ldq, pt, ldt, width, pc, pl, tokens,
+             batch, heads, max_q, max_kv, sm_scale, causal, window, out.data_ptr(), ldo, pw or None, nbytes)
     return out
 
 
 # ------------------------------------------------------------ 4-bit matvec
 
 def _w4_args(X, W, bias, out):
-    ldx = _operand(X, "X", _BF16) // 2
-    ldw = _operand(W, "W", (torch.uint8,))
-    M, K = X.shape
-    N = W.shape[0]
-    if W.shape[1] * 2 != K:
-        raise ValueError(f"X is [M, K={K}] but W holds {2 * W.shape[1]} weights a row")
+    (M, K), ldx = _rows(X, "X")
+    (N, row), ldw = _rows(W, "W", (torch.uint8,))
+    if row * 2 != K:
+        raise ValueError(f"X is [M, K={K}] but W holds {2 * row} weights a row")
     device = X.device
-    _vector(bias, "bias", N, _BF16)
-    _same_device(device, W, bias)
+    if W.device != device:
+        raise ValueError(f"W must be on {device}, found on {W.device}")
+    pb = None if bias is None else _vec(bias, "bias", N, device)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-    elif (tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or out.device != device
-          or (N > 1 and out.stride(1) != 1)):
-        raise ValueError(f"out must be bfloat16 [{M}, {N}] with unit stride along N on {device}")
-    return ldx, ldw if N > 1 else ldw + (-ldw) % 16, M, N, K, out, out.stride(0) if M > 1 else N
+        out, ldy = _empty((M, N), dtype=torch.bfloat16, device=device), N
+    else:
+        oshape, ldy = _rows(out, "out", (torch.bfloat16,))
+        if tuple(oshape) != (M, N) or out.device != device:
+            raise ValueError(f"out must be bfloat16 [{M}, {N}] with unit stride along N on {device}")
+    return device, X.data_ptr(), ldx, W.data_ptr(), ldw if N > 1 else row + (-row) % 16, M, N, K, pb, out, ldy
 
 
 def _w4_table(t, name, shape, dtypes, device):
     if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be {dtypes} {shape}, contiguous, on {device}")
+    return t.data_ptr()
 
 
 def qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None, stream=None):
     """bf16 X [M, K] (M <= 64) times int4 weights W uint8 [N, K/2] with bf16
     scales and uint8 zero points (8 where None) per group: both
     [N, K/group], group 32, 64 or 128 -> bf16 [M, N]."""
-    ldx, ldw, M, N, K, out, ldy = _w4_args(X, W, bias, out)
+    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out)
     groups = scales.shape[1] if scales.dim() == 2 else 0
     if groups == 0 or K % groups:
         raise ValueError(f"scales must be [{N}, K/group], got {tuple(scales.shape)} for K={K}")
-    _w4_table(scales, "scales", (N, groups), _BF16, X.device)
-    if zeros is not None:
-        _w4_table(zeros, "zeros", (N, groups), (torch.uint8,), X.device)
-    with torch.cuda.device(X.device):
-        _check(lib().qgemm_w4_matvec_i4(_ptr(X), ldx, _ptr(W), ldw, _ptr(scales), _ptr(zeros), K // groups, _ptr(bias),
-                                        _ptr(out), ldy, M, N, K, _stream(X.device, stream)))
+    ps = _w4_table(scales, "scales", (N, groups), _BF16, device)
+    pz = None if zeros is None else _w4_table(zeros, "zeros", (N, groups), (torch.uint8,), device)
+    _enqueue(lib().qgemm_w4_matvec_i4, device, stream, px, ldx, pw, ldw, ps, pz, K // groups, pb, out.data_ptr(), ldy,
+             M, N, K)
     return out
+
+
+_UE8M0 = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
 
 
 def qgemm_w4_matvec_mx(X, W, scale_b, b_layout, bias=None, out=None, stream=None):
     """bf16 X [M, K] (M <= 64) times the MXFP4 B operand of qgemm_mx: W uint8
     [N, K/2] e2m1, scale_b ue8m0 [N, K/32] (b_layout 1) or [ceil(N/32), K/32]
     (b_layout 32) -> bf16 [M, N]."""
-    ldx, ldw, M, N, K, out, ldy = _w4_args(X, W, bias, out)
+    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out)
     rows = -(-N // b_layout) if b_layout in (1, 32) else N
-    sdt = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
-    _w4_table(scale_b, "scale_b", (rows, K // 32), sdt, X.device)
-    with torch.cuda.device(X.device):
-        _check(lib().qgemm_w4_matvec_mx(_ptr(X), ldx, _ptr(W), ldw, _ptr(scale_b), b_layout, _ptr(bias), _ptr(out),
-                                        ldy, M, N, K, _stream(X.device, stream)))
+    ps = _w4_table(scale_b, "scale_b", (rows, K // 32), _UE8M0, device)
+    _enqueue(lib().qgemm_w4_matvec_mx, device, stream, px, ldx, pw, ldw, ps, b_layout, pb, out.data_ptr(), ldy, M, N,
+             K)
     return out
