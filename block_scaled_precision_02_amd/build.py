@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libqgemm.so")
 SOURCES = ["qgemm_api.cpp", "qgemm_i8.hip", "qgemm_f8.hip", "qgemm_mx8.hip", "qgemm_mx4.hip", "qgemm_f8b.hip", "qgemm_mx84.hip", "qgemm_mx48.hip", "qgemm_mx4h.hip", "qgemm_mx6.hip",
            "qgemm_quant.hip", "qgemm_pack.hip",
            "layer/layer_api.cpp", "layer/norm.hip", "layer/kv8_append.hip",
-           "layer/kv8_stream.hip", "layer/w4_matvec.hip"]
+           "layer/kv8_stream.hip", "layer/kv8_tile.hip", "layer/w4_matvec.hip"]
 # Per-source extra flags.  The blockscale kernel folds its MFMA partial sums
 # into the totals with VALU FMAs every 128 K elements; keeping the MFMA
 # results in VGPRs (rather than the accumulator registers, which the VALU

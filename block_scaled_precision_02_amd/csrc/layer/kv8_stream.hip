@@ -329,7 +329,13 @@ hipError_t launch_nt(const Kv8Attn &a, hipStream_t s)
         hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, 4, KV8_E4M3>), grid, dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, 4, KV8_I8>), grid, dim3(256), 0, s, a);
-    hipError_t e = hipGetLastError();
+    return hipGetLastError();
+}
+
+template <int DC>
+hipError_t launch_dim(const Kv8Attn &a, hipStream_t s)
+{
+    hipError_t e = a.kernel == 1 ? launch_kv8_tile(a, s) : a.nt == 1 ? launch_nt<DC, 1>(a, s) : launch_nt<DC, 2>(a, s);
     if (e == hipSuccess && a.splits > 1) {
         const dim3 join((unsigned)a.max_q, (unsigned)((a.kv_heads * a.group + 3) / 4), (unsigned)a.batch);
         hipLaunchKernelGGL((kv8_join_kernel<DC>), join, dim3(256), 0, s, a);
@@ -338,32 +344,36 @@ hipError_t launch_nt(const Kv8Attn &a, hipStream_t s)
     return e;
 }
 
-template <int DC>
-hipError_t launch_dim(const Kv8Attn &a, hipStream_t s)
-{
-    return a.nt == 1 ? launch_nt<DC, 1>(a, s) : launch_nt<DC, 2>(a, s);
-}
-
 }  // namespace
 
 int64_t kv8_plan(Kv8Attn &a)
 {
     const int64_t rows = (int64_t)a.max_q * a.group;
-    a.kernel = 0;
-    a.nt = rows > 16 ? 2 : 1;
-    a.row_tiles = (int)((rows + 16 * a.nt - 1) / (16 * a.nt));
     // steps that a row tile can cover; a window starts anywhere in its first one
     int64_t steps = ((int64_t)a.max_kv + STEP - 1) / STEP;
     if (a.causal && a.window > 0)
         steps = std::min(steps, ((int64_t)a.window + a.max_q + 2 * STEP - 2) / STEP);
     steps = std::max<int64_t>(steps, 1);
-    const int64_t units = (int64_t)a.row_tiles * a.kv_heads * a.batch;
-    int64_t want = (2048 + units - 1) / units;
-    int64_t per = (steps + want - 1) / want;
-    per = per < 4 ? 4 : (per + 3) / 4 * 4;
-    if (steps <= 8)
-        per = steps;
-    a.split_steps = (int)per;
+    int64_t want, per;
+    if (rows > 32) {
+        a.kernel = 1;
+        a.waves = rows > 128 && a.dim <= 128 ? 8 : 4;
+        a.row_tiles = (int)((rows + 32 * a.waves - 1) / (32 * a.waves));
+        const int64_t units = (int64_t)a.row_tiles * a.kv_heads * a.batch;
+        want = units >= 256 ? 1 : (256 + units - 1) / units;
+        per = std::max<int64_t>((steps + want - 1) / want, 8);
+    } else {
+        a.kernel = 0;
+        a.nt = rows > 16 ? 2 : 1;
+        a.row_tiles = (int)((rows + 16 * a.nt - 1) / (16 * a.nt));
+        const int64_t units = (int64_t)a.row_tiles * a.kv_heads * a.batch;
+        want = (2048 + units - 1) / units;
+        per = (steps + want - 1) / want;
+        per = per < 4 ? 4 : (per + 3) / 4 * 4;
+        if (steps <= 8)
+            per = steps;
+    }
+    a.split_steps = (int)std::min(per, steps);
     a.splits = (int)((steps + per - 1) / per);
     if (a.splits == 1)
         return 0;

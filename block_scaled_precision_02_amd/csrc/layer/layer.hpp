@@ -45,12 +45,14 @@ struct Kv8Attn {
     // the plan (kv8_plan)
     int kernel;                       // 0 streaming (few rows), 1 tiled (many rows)
     int nt;                           // streaming: 16-row tiles a wave
+    int waves;                        // tiled: waves of 32 rows a workgroup
     int row_tiles;                    // of the longest sequence, per kv head
-    int split_steps, splits;          // streaming: steps of 64 tokens a split, splits
+    int split_steps, splits;          // steps of 64 tokens a split, splits
 };
 // Fills the plan; returns the workspace bytes it needs.
 int64_t kv8_plan(Kv8Attn &a);
 hipError_t launch_kv8_attention(const Kv8Attn &a, hipStream_t s);
+hipError_t launch_kv8_tile(const Kv8Attn &a, hipStream_t s);   // the tiled kernel alone
 
 // bf16 rows times 4-bit weights (M <= 64).
 struct W4Args {

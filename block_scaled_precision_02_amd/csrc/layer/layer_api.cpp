@@ -267,7 +267,7 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
             return fail(QGEMM_ERR_BAD_LAYOUT, "workspace of %lld bytes: need %lld, 16-byte aligned",
                         (long long)workspace_bytes, (long long)need);
     }
-    if ((int64_t)a.row_tiles * a.splits * 256 >= (LD_LIMIT << 1) || max_q * 256 >= (LD_LIMIT << 1))
+    if ((int64_t)a.row_tiles * a.splits >= 65536 || max_q * 256 >= (LD_LIMIT << 1))
         return fail(QGEMM_ERR_BAD_SHAPE, "max_q=%lld with %lld heads is too large for one call", (long long)max_q,
                     (long long)heads);
     TRY(check_device());
