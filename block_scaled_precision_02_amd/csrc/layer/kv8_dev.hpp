@@ -23,6 +23,9 @@ __device__ __forceinline__ u32x2 codes4_bf16(unsigned w)
         const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
         return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
     } else {
+        // (the compiler would take the dword apart where it is loaded, and hold
+        // four registers for one until it is used)
+        asm("" : "+v"(w));
         // an int8 has at most 7 significant bits besides its sign: the upper
         // half of its binary32 form is the bf16 value
         const unsigned a = __float_as_uint((float)(int8_t)w), b = __float_as_uint((float)(int8_t)(w >> 8));
@@ -48,6 +51,7 @@ __device__ __forceinline__ u32x2 codes4_f16(unsigned w)
         const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
         return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
     } else {
+        asm("" : "+v"(w));
         const auto lo = __builtin_amdgcn_cvt_pkrtz((float)(int8_t)w, (float)(int8_t)(w >> 8));
         const auto hi = __builtin_amdgcn_cvt_pkrtz((float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24));
         return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};

@@ -46,11 +46,30 @@ namespace {
 constexpr int STEP = 64;
 constexpr float NEG_INF = -__builtin_inff();
 
-__device__ __forceinline__ float xor16(float v) { return __shfl_xor(v, 16); }
-__device__ __forceinline__ float xor32(float v) { return __shfl_xor(v, 32); }
+// max / sum over the four lane groups
+__device__ __forceinline__ float groups_max(float v)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float groups_sum(float v)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Waves a SIMD that the registers are held to.
+constexpr int stream_occupancy(int dc, int nt)
+{
+    return nt == 1 ? (dc == 1 ? 4 : dc <= 3 ? 2 : 1) : dc <= 2 ? 2 : 1;
+}
 
 template <int DC, int NT, int WAVES, int FMT>
-__global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
+__global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stream_kernel(Kv8Attn a)
 {
     constexpr int D = DC * 64, DT = D / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -102,35 +121,51 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
             o[t][d] = f32x4{0, 0, 0, 0};
     }
 
-    // this lane's K rows of a step: tokens 16 kg + 4 j + (lane & 3)
+    // this lane's K rows of a step: tokens 16 kg + 4 j + (lane & 3); its V tokens
+    // and scales: 16 g .. 16 g + 15.  K's registers take the next step as soon as
+    // the first product is done, V's after the second: one or the other is always
+    // under way.  Block numbers come a step earlier still.
     const int kg = n16 >> 2;
-    for (int s = s0 + wave; s < s1; s += WAVES) {
-        const int base = s * STEP;
-        // the block of a 16-token group, or -1 where no row sees it
-        const auto block_at = [&](int tok) {
-            int id = -1;
-            if (tok < hi_all && tok + 16 > lo_all)
-                id = table[tok >> bshift];
-            return (unsigned)id < (unsigned)a.blocks ? id : -1;
-        };
-        const int ktok = base + 16 * kg, vtok = base + 16 * g;
-        const int kid = block_at(ktok), vid = block_at(vtok);
-        const int64_t kunit = (int64_t)max(kid, 0) * a.kv_heads + head, vunit = (int64_t)max(vid, 0) * a.kv_heads + head;
-        const uint8_t *kp = a.ck + kunit * unit_bytes + (int64_t)((ktok & (a.bs - 1)) + (lane & 3)) * D + 16 * g;
-        const uint8_t *vp = a.cv + vunit * unit_bytes + (int64_t)n16 * a.bs + (vtok & (a.bs - 1));
-        u32x4 kw[4][DC], vw[DT];
+    const auto block_at = [&](int tok) {   // -1 where no row sees the 16 tokens from tok on
+        int id = -1;
+        if (tok < hi_all && tok + 16 > lo_all)
+            id = table[tok >> bshift];
+        return (unsigned)id < (unsigned)a.blocks ? id : -1;
+    };
+    u32x4 kw[4][DC], vw[DT];
+    float sk = 0.0f, raw = 0.0f;
+    const auto load_k = [&](int s, int id) {
+        const int tok = s * STEP + 16 * kg;
+        const int64_t unit = (int64_t)max(id, 0) * a.kv_heads + head;
+        const uint8_t *p = a.ck + unit * unit_bytes + (int64_t)((tok & (a.bs - 1)) + (lane & 3)) * D + 16 * g;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int c = 0; c < DC; ++c)
-                kw[j][c] = *(const u32x4 *)(kp + 4 * j * D + 64 * c);
+                kw[j][c] = *(const u32x4 *)(p + 4 * j * D + 64 * c);
+    };
+    const auto load_v = [&](int s, int id) {
+        const int tok = s * STEP + 16 * g;
+        const int64_t unit = (int64_t)max(id, 0) * a.kv_heads + head;
+        const uint8_t *p = a.cv + unit * unit_bytes + (int64_t)n16 * a.bs + (tok & (a.bs - 1));
+        sk = a.sk[unit];
+        raw = a.sv[unit];
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-            vw[d] = *(const u32x4 *)(vp + (int64_t)(16 * d) * a.bs);
-        const float sk = vid >= 0 ? a.sk[vunit] * a.scale2 : 0.0f;
-        const float raw = vid >= 0 ? a.sv[vunit] : 0.0f;
-        const VScale sv = v_scale(raw, held);
-
+            vw[d] = *(const u32x4 *)(p + (int64_t)(16 * d) * a.bs);
+    };
+    int vid = -1, next_k = -1, next_v = -1;
+    if (s0 + wave < s1) {
+        const int s = s0 + wave;
+        const int kid = block_at(s * STEP + 16 * kg);
+        vid = block_at(s * STEP + 16 * g);
+        load_k(s, kid);
+        load_v(s, vid);
+        next_k = block_at((s + WAVES) * STEP + 16 * kg);
+        next_v = block_at((s + WAVES) * STEP + 16 * g);
+    }
+    for (int s = s0 + wave; s < s1; s += WAVES) {
+        const int base = s * STEP, vtok = base + 16 * g;
         f32x4 sc[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -149,10 +184,16 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
                     sc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[t][2 * c + 1], sc[t][j], 0, 0, 0);
                 }
             }
+        const bool more = s + WAVES < s1;
+        if (more)
+            load_k(s + WAVES, next_k);
+        // (a scale of a block that is not there may be anything)
+        const float k_scale = vid >= 0 ? sk * a.scale2 : 0.0f, v_raw = vid >= 0 ? raw : 0.0f;
+        const VScale sv = v_scale(v_raw, held);
 
         // a step that every row sees whole needs no mask; elsewhere the codes
         // of V that no row sees (0 * NaN), or whose scale is zero, are cleared
-        const bool whole = base >= lo_in && base + STEP <= hi_in && __all(raw > 0.0f);
+        const bool whole = base >= lo_in && base + STEP <= hi_in && __all(v_raw > 0.0f);
         if (!whole) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -160,7 +201,7 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = vtok + 4 * k + i;
-                    if (raw > 0.0f && tok >= lo_all && tok < hi_all)
+                    if (v_raw > 0.0f && tok >= lo_all && tok < hi_all)
                         keep |= 0xffu << (8 * i);
                 }
 #pragma unroll
@@ -176,7 +217,7 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    x[4 * j + i] = fmaf(sc[t][j][i], sk, sv.log2);
+                    x[4 * j + i] = fmaf(sc[t][j][i], k_scale, sv.log2);
             if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -187,8 +228,7 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
 #pragma unroll
             for (int i = 1; i < 16; ++i)
                 top = fmaxf(top, x[i]);
-            top = fmaxf(top, xor16(top));
-            top = fmaxf(top, xor32(top));
+            top = groups_max(top);
             const float now = fmaxf(m[t], top);
             const float ref = now == NEG_INF ? 0.0f : now;
             const float fade = __builtin_amdgcn_exp2f(m[t] - ref), zero = ref - W_TOP;
@@ -225,6 +265,12 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
                 o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][d], 0, 0, 0);
             }
         }
+        if (more) {
+            load_v(s + WAVES, next_v);
+            vid = next_v;
+            next_k = block_at((s + 2 * WAVES) * STEP + 16 * kg);
+            next_v = block_at((s + 2 * WAVES) * STEP + 16 * g);
+        }
     }
 
     // join the waves, a tile at a time: in LDS, [wave][row][D + 4], and the
@@ -234,9 +280,7 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
     __shared__ float om[WAVES][16], ol[WAVES][16];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        float sum = l[t];
-        sum += xor16(sum);
-        sum += xor32(sum);
+        const float sum = groups_sum(l[t]);
         if (t)
             __syncthreads();
         if (g == 0) {
@@ -286,14 +330,16 @@ __global__ void __launch_bounds__(WAVES * 64) kv8_stream_kernel(Kv8Attn a)
     }
 }
 
-// The splits of one row joined: a wave a row.
-template <int DC>
+// The splits of one row joined: WPR waves a row, taking turns over the splits,
+// in a fixed order.
+template <int DC, int WPR>
 __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
 {
     constexpr int D = DC * 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    [[maybe_unused]] __shared__ float part_o[WPR][D], part_l[WPR];
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wid % WPR;
     const int heads = a.kv_heads * a.group;
-    const int b = blockIdx.z, hq = blockIdx.y * 4 + wave, t = blockIdx.x;
+    const int b = blockIdx.z, hq = blockIdx.y * (4 / WPR) + wid / WPR, t = blockIdx.x;
     const int c0 = a.cu[b], q = a.cu[b + 1] - c0;
     if (hq >= heads || t >= q || c0 < 0 || (int64_t)c0 + q > a.tokens)
         return;
@@ -307,29 +353,58 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
         top = fmaxf(top, __shfl_xor(top, off));
     const float ref = top == NEG_INF ? 0.0f : top;
     float all = 0.0f, acc[DC] = {};
-    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+    for (int s = wave; s < a.splits; s += WPR) {
         const float f = __builtin_amdgcn_exp2f(stat[2 * s] - ref);
         all = fmaf(stat[2 * s + 1], f, all);
 #pragma unroll
         for (int i = 0; i < DC; ++i)
             acc[i] = fmaf(part[(int64_t)s * D + i], f, acc[i]);
     }
-    const float inv = all > 0.0f ? 1.0f / all : 0.0f;
-    uint16_t *o = a.O + (int64_t)(c0 + t) * a.ldo + hq * D + lane * DC;
+    uint16_t *out = a.O + (int64_t)(c0 + t) * a.ldo + hq * D;
+    if constexpr (WPR == 1) {
+        const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+#pragma unroll
+        for (int i = 0; i < DC; ++i)
+            out[lane * DC + i] = (uint16_t)pack_bf16(acc[i] * inv, 0.0f);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < DC; ++i)
-        o[i] = (uint16_t)pack_bf16(acc[i] * inv, 0.0f);
+        part_o[wave][lane * DC + i] = acc[i];
+    if (lane == 0)
+        part_l[wave] = all;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        const int d = threadIdx.x;
+        float l = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            l += part_l[w];
+            v += part_o[w][d];
+        }
+        out[d] = (uint16_t)pack_bf16(l > 0.0f ? v / l : 0.0f, 0.0f);
+    }
+}
+
+template <int DC, int NT, int WAVES>
+hipError_t launch_waves(const Kv8Attn &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.row_tiles * a.splits), (unsigned)a.kv_heads, (unsigned)a.batch);
+    if (a.fmt == KV8_E4M3)
+        hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, WAVES, KV8_E4M3>), grid, dim3(WAVES * 64), 0, s, a);
+    else
+        hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, WAVES, KV8_I8>), grid, dim3(WAVES * 64), 0, s, a);
+    return hipGetLastError();
 }
 
 template <int DC, int NT>
 hipError_t launch_nt(const Kv8Attn &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.row_tiles * a.splits), (unsigned)a.kv_heads, (unsigned)a.batch);
-    if (a.fmt == KV8_E4M3)
-        hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, 4, KV8_E4M3>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((kv8_stream_kernel<DC, NT, 4, KV8_I8>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    if constexpr (stream_occupancy(DC, NT) > 1)
+        if (a.waves == 8)
+            return launch_waves<DC, NT, 8>(a, s);
+    return launch_waves<DC, NT, 4>(a, s);
 }
 
 template <int DC>
@@ -337,8 +412,13 @@ hipError_t launch_dim(const Kv8Attn &a, hipStream_t s)
 {
     hipError_t e = a.kernel == 1 ? launch_kv8_tile(a, s) : a.nt == 1 ? launch_nt<DC, 1>(a, s) : launch_nt<DC, 2>(a, s);
     if (e == hipSuccess && a.splits > 1) {
-        const dim3 join((unsigned)a.max_q, (unsigned)((a.kv_heads * a.group + 3) / 4), (unsigned)a.batch);
-        hipLaunchKernelGGL((kv8_join_kernel<DC>), join, dim3(256), 0, s, a);
+        const unsigned heads = (unsigned)(a.kv_heads * a.group);
+        if (a.splits > 4)
+            hipLaunchKernelGGL((kv8_join_kernel<DC, 4>), dim3((unsigned)a.max_q, heads, (unsigned)a.batch), dim3(256), 0,
+                               s, a);
+        else
+            hipLaunchKernelGGL((kv8_join_kernel<DC, 1>), dim3((unsigned)a.max_q, (heads + 3) / 4, (unsigned)a.batch),
+                               dim3(256), 0, s, a);
         e = hipGetLastError();
     }
     return e;
@@ -354,26 +434,36 @@ int64_t kv8_plan(Kv8Attn &a)
     if (a.causal && a.window > 0)
         steps = std::min(steps, ((int64_t)a.window + a.max_q + 2 * STEP - 2) / STEP);
     steps = std::max<int64_t>(steps, 1);
-    int64_t want, per;
-    if (rows > 32) {
-        a.kernel = 1;
-        a.waves = rows > 128 && a.dim <= 128 ? 8 : 4;
-        a.row_tiles = (int)((rows + 32 * a.waves - 1) / (32 * a.waves));
-        const int64_t units = (int64_t)a.row_tiles * a.kv_heads * a.batch;
-        want = units >= 256 ? 1 : (256 + units - 1) / units;
-        per = std::max<int64_t>((steps + want - 1) / want, 8);
-    } else {
-        a.kernel = 0;
-        a.nt = rows > 16 ? 2 : 1;
-        a.row_tiles = (int)((rows + 16 * a.nt - 1) / (16 * a.nt));
-        const int64_t units = (int64_t)a.row_tiles * a.kv_heads * a.batch;
-        want = (2048 + units - 1) / units;
-        per = (steps + want - 1) / want;
-        per = per < 4 ? 4 : (per + 3) / 4 * 4;
-        if (steps <= 8)
-            per = steps;
+    // Waves a workgroup and splits: the fewest turns of the loop over steps from
+    // first to last, with the workgroups that are resident together as one round;
+    // a workgroup's start and end count as `ends` turns, joining splits as `ends`
+    // more.  (Single tokens: 64 x 8192 tokens, 512 units: no split 157 us, two
+    // 169, four 184; 131072 tokens, 8 units: splits of 32 steps 58 us, of 16 60,
+    // of 8 67.)
+    a.kernel = rows > 32;
+    a.nt = rows > 16 ? 2 : 1;
+    const int dc = a.dim / 64, ends = a.kernel ? 4 : 1;
+    int64_t best = -1, per = steps;
+    for (int waves = 8; waves >= 4; waves -= 4) {
+        const int per_cu = 4 * (a.kernel ? kv8_tile_occupancy(dc, waves) : stream_occupancy(dc, a.nt)) / waves;
+        if (per_cu == 0)
+            continue;
+        const int tile_rows = a.kernel ? 32 * waves : 16 * a.nt;
+        const int64_t tiles = (rows + tile_rows - 1) / tile_rows, units = tiles * a.kv_heads * a.batch;
+        for (int64_t w = 1; w <= 64 && w <= steps; ++w) {
+            if (a.kernel && w > 1 && units * w > 256 * per_cu)
+                break;   // many rows: their sums cost more than an uneven last round
+            const int64_t p = (steps + w - 1) / w, turns = a.kernel ? p : (p + waves - 1) / waves;
+            const int64_t cost = (units * w + 256 * per_cu - 1) / (256 * per_cu) * (turns + ends) + (w > 1 ? ends : 0);
+            if (best < 0 || cost < best) {
+                best = cost;
+                per = p;
+                a.waves = waves;
+                a.row_tiles = (int)tiles;
+            }
+        }
     }
-    a.split_steps = (int)std::min(per, steps);
+    a.split_steps = (int)per;
     a.splits = (int)((steps + per - 1) / per);
     if (a.splits == 1)
         return 0;

@@ -56,8 +56,11 @@ __device__ __forceinline__ int k_chunk(int row, int c)
 }
 __device__ __forceinline__ int v_chunk(int row, int c) { return row * 8 + (c ^ ((row >> 1) & 7)); }
 
+// Waves a SIMD that the registers are held to.
+constexpr int tile_occupancy(int dc, int) { return dc == 1 ? 3 : dc == 2 ? 2 : 1; }
+
 template <int DC, int WAVES, int FMT>
-__global__ void __launch_bounds__(WAVES * 64) kv8_tile_kernel(Kv8Attn a)
+__global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_tile_kernel(Kv8Attn a)
 {
     constexpr int D = DC * 64, DT = D / 32, KS = D / 16, CH = D / 8;
     constexpr int THREADS = WAVES * 64, PIECES = STEP * D / 16;        // of 16 codes, of K and of V, a step
@@ -332,10 +335,18 @@ hipError_t launch_waves(const Kv8Attn &a, hipStream_t s)
 
 }  // namespace
 
+int kv8_tile_occupancy(int dc, int waves)
+{
+    // eight waves, a step's codes shared by 256 rows: D = 128 (4096 tokens over
+    // 8192: 512 us against 541 with four; D = 64: 104 against 75, 5 prompts of
+    // up to 1777 tokens, where three workgroups of four are resident)
+    return waves == 4 || (waves == 8 && dc == 2) ? tile_occupancy(dc, waves) : 0;
+}
+
 hipError_t launch_kv8_tile(const Kv8Attn &a, hipStream_t s)
 {
     switch (a.dim) {
-    case 64: return a.waves == 8 ? launch_waves<1, 8>(a, s) : launch_waves<1, 4>(a, s);
+    case 64: return launch_waves<1, 4>(a, s);
     case 128: return a.waves == 8 ? launch_waves<2, 8>(a, s) : launch_waves<2, 4>(a, s);
     case 192: return launch_waves<3, 4>(a, s);
     default: return launch_waves<4, 4>(a, s);

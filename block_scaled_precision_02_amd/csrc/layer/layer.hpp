@@ -45,7 +45,7 @@ struct Kv8Attn {
     // the plan (kv8_plan)
     int kernel;                       // 0 streaming (few rows), 1 tiled (many rows)
     int nt;                           // streaming: 16-row tiles a wave
-    int waves;                        // tiled: waves of 32 rows a workgroup
+    int waves;                        // waves a workgroup (tiled: of 32 rows each)
     int row_tiles;                    // of the longest sequence, per kv head
     int split_steps, splits;          // steps of 64 tokens a split, splits
 };
@@ -53,6 +53,9 @@ struct Kv8Attn {
 int64_t kv8_plan(Kv8Attn &a);
 hipError_t launch_kv8_attention(const Kv8Attn &a, hipStream_t s);
 hipError_t launch_kv8_tile(const Kv8Attn &a, hipStream_t s);   // the tiled kernel alone
+// Waves a SIMD that it is built for, by head_dim / 64 and waves a workgroup; 0:
+// not built.
+int kv8_tile_occupancy(int dc, int waves);
 
 // bf16 rows times 4-bit weights (M <= 64).
 struct W4Args {
