@@ -20,13 +20,15 @@ namespace qgemm {
 namespace {
 
 constexpr int AP_THREADS = 256;
-constexpr int AP_KEEP = 4;   // 16-byte pieces of new rows a thread keeps
+constexpr int AP_KEEP = 2;   // 16-byte pieces of new rows a thread keeps
 
 // x / s, correctly rounded: with inv the correctly rounded reciprocal, a
 // residual step on a quotient within a unit in the last place gives the
 // rounded one (Markstein, 1990), while nothing leaves the normal range; else
 // the division itself.  x * inv alone can be off by more than a unit, so that
-// it takes two steps.  The residual of a zero is +0: the sign is x's.
+// it takes two steps.  The residual of a zero is +0: the sign is x's (SIGNED:
+// the code keeps a zero's).
+template <bool SIGNED>
 struct Divider {
     float s, inv;
     bool fast;
@@ -42,19 +44,20 @@ struct Divider {
             return x / s;
         float q = x * inv;
         q = fmaf(fmaf(-q, s, x), inv, q);
-        return __builtin_copysignf(fmaf(fmaf(-q, s, x), inv, q), x);
+        q = fmaf(fmaf(-q, s, x), inv, q);
+        return SIGNED ? __builtin_copysignf(q, x) : q;
     }
 };
 
 template <int FMT>
-__device__ __forceinline__ u32x2 enc_piece(u32x4 w, const Divider &d)
+__device__ __forceinline__ u32x2 enc_piece(u32x4 w, const Divider<FMT == KV8_E4M3> &d)
 {
     return u32x2{enc4<FMT>(d(lo_bf16(w[0])), d(hi_bf16(w[0])), d(lo_bf16(w[1])), d(hi_bf16(w[1]))),
                  enc4<FMT>(d(lo_bf16(w[2])), d(hi_bf16(w[2])), d(lo_bf16(w[3])), d(hi_bf16(w[3])))};
 }
 
 template <int FMT>
-__device__ __forceinline__ unsigned requantise(unsigned w, float was, const Divider &d)
+__device__ __forceinline__ unsigned requantise(unsigned w, float was, const Divider<FMT == KV8_E4M3> &d)
 {
     float v[4];
     codes4_f32<FMT>(w, v);
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(Kv8Append a)
         top = fmaxf(top, wtop[w]);
     const float now = fmaxf(was, top * (FMT == KV8_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f));
     const bool grown = old > 0 && now > was;
-    const Divider div(now);
+    const Divider<FMT == KV8_E4M3> div(now);
     if (t == 0)
         *scale = now;
 
@@ -185,6 +188,15 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(Kv8Append a)
     for (int p = t + AP_THREADS * AP_KEEP; p < np; p += AP_THREADS)
         put(p, piece(p));
     __syncthreads();
+    // a few tokens whose block keeps its scale: byte stores, which wait for
+    // nothing, where reading the 16 bytes around them costs a trip to memory
+    if (!grown && n < 4) {
+        for (int i = t; i < n * D; i += AP_THREADS) {
+            const int tok = old + i / D, d = i % D;
+            codes[(int64_t)d * bs + tok] = ((const uint8_t *)(stage + tok * PITCH))[d];
+        }
+        return;
+    }
     // item: four channels of 16 tokens; the tokens of a row of the block on
     // neighbouring lanes
     const int groups = bs / 16, lo_b = old, hi_b = old + n;

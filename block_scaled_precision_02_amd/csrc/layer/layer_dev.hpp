@@ -46,14 +46,17 @@ __device__ __forceinline__ unsigned enc4_e4m3(float a, float b, float c, float d
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-// Four int8 codes, nearest even, clamped to +-127.
+// Four int8 codes, nearest even, clamped to +-127: added to 3 * 2^22, a value
+// is rounded to a whole number whose low byte is the code.
 __device__ __forceinline__ unsigned enc4_i8(float a, float b, float c, float d)
 {
-    const int ia = (int)__builtin_rintf(__builtin_amdgcn_fmed3f(a, -127.0f, 127.0f));
-    const int ib = (int)__builtin_rintf(__builtin_amdgcn_fmed3f(b, -127.0f, 127.0f));
-    const int ic = (int)__builtin_rintf(__builtin_amdgcn_fmed3f(c, -127.0f, 127.0f));
-    const int id = (int)__builtin_rintf(__builtin_amdgcn_fmed3f(d, -127.0f, 127.0f));
-    return (ia & 0xff) | ((ib & 0xff) << 8) | ((ic & 0xff) << 16) | ((unsigned)id << 24);
+    constexpr float ROUND = 12582912.0f;
+    const unsigned ia = __float_as_uint(__builtin_amdgcn_fmed3f(a, -127.0f, 127.0f) + ROUND);
+    const unsigned ib = __float_as_uint(__builtin_amdgcn_fmed3f(b, -127.0f, 127.0f) + ROUND);
+    const unsigned ic = __float_as_uint(__builtin_amdgcn_fmed3f(c, -127.0f, 127.0f) + ROUND);
+    const unsigned id = __float_as_uint(__builtin_amdgcn_fmed3f(d, -127.0f, 127.0f) + ROUND);
+    const unsigned lo = __builtin_amdgcn_perm(ib, ia, 0x0c0c0400u), hi = __builtin_amdgcn_perm(id, ic, 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
 // Eight e2m1 codes in a dword, element i in bits 4i .. 4i+3 (the conversion

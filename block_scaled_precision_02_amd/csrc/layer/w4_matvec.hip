@@ -494,12 +494,25 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
     }
 }
 
+template <int GROUP, int MT, int RI, int NT>
+hipError_t launch_tiles(const W4Args &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, NT>), dim3((unsigned)((a.N + 16 * NT - 1) / (16 * NT))),
+                       dim3(W4_WAVES * 64), 0, s, a);
+    return hipGetLastError();
+}
+
 template <int GROUP, int MT, int RI>
 hipError_t launch_wide(const W4Args &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, 1>), dim3((unsigned)((a.N + 15) / 16)), dim3(W4_WAVES * 64), 0,
-                       s, a);
-    return hipGetLastError();
+    // two tiles of weights a wave halve the loads of x, where that leaves a
+    // workgroup a CU (MXFP4, 64 rows, 8192x8192: 42 us against 67; 32 rows,
+    // 2112x7168: 23 against 19)
+    if constexpr (MT > 1) {
+        if (a.N >= 8192)
+            return launch_tiles<GROUP, MT, RI, 2>(a, s);
+    }
+    return launch_tiles<GROUP, MT, RI, 1>(a, s);
 }
 
 template <int GROUP, int XR, int CPW>
