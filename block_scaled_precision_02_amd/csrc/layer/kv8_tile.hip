@@ -16,6 +16,11 @@
 //  * the running maximum moves only when a weight would pass 2^15 (a binary16's
 //    range): weights are 2^(x - reference + 7) with the reference up to 2^8 out
 //    of date, and most steps neither fade the sums nor touch the accumulators.
+// On one MI355X: a chunk of 4096 tokens over 8192, 32 heads over 8 of 128, e4m3,
+// 512 us, 806 TFLOP/s (a bf16 library product of 8192^3: 1323); five prompts of
+// up to 1777 tokens, 16 heads of 64, int8, window 1024, 74 us, 310 TFLOP/s, where
+// the exponentials weigh twice as much; 192 and 256 channels, whose accumulators
+// leave one wave a SIMD and nothing to run beside its softmax, 250 to 270.
 // The rows of a kv head (its tokens times the heads that share it) are cut into
 // tiles of 32 a wave; a split of the keys, where there are few tiles, leaves
 // sums for kv8_join_kernel.
