@@ -238,7 +238,9 @@ def _sequences(table, cu, lens, device):
     if len(tshape) != 2 or tshape[0] != batch or (tshape[1] > 1 and tstride[1] != 1):
         raise ValueError(f"block_table must be [{batch}, blocks] with unit stride along its rows, got {tuple(tshape)}")
     width = tshape[1]
-    ldt = tstride[0] if batch > 1 and tstride[0] > width else width
+    ldt = tstride[0] if batch > 1 else width
+    if ldt < width:
+        raise ValueError(f"block_table rows must not overlap: stride {ldt}, {width} entries")
     return table.data_ptr(), ldt, width, cu.data_ptr(), lens.data_ptr(), batch
 
 
@@ -288,6 +290,9 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
         if nbytes > 0:
             workspace = _empty(nbytes, dtype=torch.uint8, device=device)
             pw = workspace.data_ptr()
+            if stream is not None:   # it is let go here, when the stream may not have come to it
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                        torch.cuda.ExternalStream(int(stream), device=device))
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     else:

@@ -346,3 +346,53 @@ def test_python_refusals():
         q.qgemm_kv8_append(cache, Q, Q, table, cu, lens, 3)               # 4 heads into 2
     with pytest.raises(ValueError):
         q.KV8Cache(cache.k, cache.v.transpose(2, 3).contiguous(), cache.k_scale, cache.v_scale)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_own_workspace_outlives_a_given_stream(raw):
+    """The workspace that a call allocates for itself is not handed out again
+    while the given stream may still use it: calls in a row, each on a stream
+    that starts late, with the current stream taking and writing memory of the
+    same size in between."""
+    s = Setup("e4m3", 1, 128, 64, [(1, 9000)], seed=15)
+    cache, Q = s.gpu(), s.bf16(1, 4, 128).cuda()
+    table, cu, lens = s.seqs()
+    need = q.lib().qgemm_kv8_attention_workspace(cache._ref, 1, 1, 4, 1, 9000, 1, 0)
+    assert need > 0
+    want = q.qgemm_kv8_attention(cache, Q, table, cu, lens, 1, 9000)
+    side = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big = big * 1.0001
+        out = torch.empty_like(want)
+        q.qgemm_kv8_attention(cache, Q, table, cu, lens, 1, 9000, out=out,
+                              stream=side.cuda_stream if raw else side)
+        torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        outs.append(out)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_shared_table_rows_are_refused():
+    s = Setup("e4m3", 2, 64, 16, [(1, 20), (1, 20)], seed=1)
+    table, cu, lens = s.seqs()
+    Q = s.bf16(2, 4, 64).cuda()
+    one = table[:1].expand(2, -1)
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_attention(s.gpu(), Q, one, cu, lens, 1, 20)
+    with pytest.raises(ValueError):
+        q.qgemm_kv8_append(s.gpu(), Q[:, :2].contiguous(), Q[:, 2:].contiguous(), one, cu, lens, 1)
+
+
+def test_nothing_to_do():
+    cache = q.KV8Cache.empty(2, 2, 64, 16)
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert q.qgemm_kv8_attention(cache, e, z(0, 3), z(1), z(0), 0, 0).shape == (0, 4, 64)
+    q.qgemm_kv8_append(cache, e[:, :2], e[:, :2], z(0, 3), z(1), z(0), 0)
+    assert q.qgemm_kv8_attention(cache, e, z(2, 3), z(3), z(2), 0, 5).shape == (0, 4, 64)
