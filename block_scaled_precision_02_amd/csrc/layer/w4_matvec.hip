@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
         int flip = 0, nth = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += step, flip ^= 1, ++nth) {
             const int next = min(tile + step, tiles - 1);
+            const bool more = tile + step < tiles;   // weights past the last tile cost 3 of 14 us at 1x8192x8192, MXFP4
             const uint8_t *w = weights(next), *sz = tab[flip];
             load_scales(next);
             // x and its sums are the same for every tile: an offset that the
@@ -435,7 +436,8 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
                 if (c >= nc)
                     break;
                 const u32x4 wc = wv[c];
-                wv[c] = load_chunk(w, c);
+                if (more)
+                    wv[c] = load_chunk(w, c);
                 const int at = (c0 + c) * SC;
                 if constexpr (MX) {
                     // a group past K (x is zero there) takes any scale of the row
@@ -523,13 +525,16 @@ hipError_t launch_cpw(const W4Args &a, hipStream_t s)
 {
     constexpr int NUM_CU = 256, KEPT = 8;   // tiles whose sums are kept, at most
     const int tiles = (a.N + 15) / 16, chunks = (a.K + CHUNK - 1) / CHUNK;
-    int wgs = XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
+    const size_t x_bytes = (size_t)W4_WAVES * CPW * 16 * XR * 16;
+    // as many workgroups as are resident: two a CU while LDS has room for both
+    // (4x8192x8192, 64 KB of x: one 14 us, two 18; 1x21504x5376: 20 and 18)
+    int wgs = x_bytes <= 32768 && XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
     if (chunks > W4_WAVES * CPW) {
         wgs = wgs > (tiles + KEPT - 1) / KEPT ? wgs : (tiles + KEPT - 1) / KEPT;
         kept = (tiles + wgs - 1) / wgs;
     }
     const dim3 grid((unsigned)(tiles < wgs ? tiles : wgs)), block(W4_WAVES * 64);
-    const size_t lds = (size_t)W4_WAVES * CPW * 16 * XR * 16 + kept * 1024;
+    const size_t lds = x_bytes + kept * 1024;
     if constexpr (GROUP != 0) {
         if (a.Z) {
             hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, true>), grid, block, lds, s, a);
