@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
     const int rows = q * a.group, row0 = tile * (16 * NT);
     if (q <= 0 || row0 >= rows || c0 < 0 || (int64_t)c0 + q > a.tokens)
         return;
-    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fffffc0)), 0);
+    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fff0000)), 0);
     const int qlen_pos = a.lens[b];   // positions go by the sequence's own length
 
     // the tile's rows and what they see

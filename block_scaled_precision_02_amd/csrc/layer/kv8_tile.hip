@@ -17,10 +17,12 @@
 //    range): weights are 2^(x - reference + 7) with the reference up to 2^8 out
 //    of date, and most steps neither fade the sums nor touch the accumulators.
 // On one MI355X: a chunk of 4096 tokens over 8192, 32 heads over 8 of 128, e4m3,
-// 512 us, 806 TFLOP/s (a bf16 library product of 8192^3: 1323); five prompts of
-// up to 1777 tokens, 16 heads of 64, int8, window 1024, 74 us, 310 TFLOP/s, where
-// the exponentials weigh twice as much; 192 and 256 channels, whose accumulators
-// leave one wave a SIMD and nothing to run beside its softmax, 250 to 270.
+// 469 us, 880 TFLOP/s (a bf16 library product of 8192^3: 1323; 512 us with the
+// block numbers loaded together with the codes, which waited for them); five
+// prompts of up to 1777 tokens, 16 heads of 64, int8, window 1024, 71 us, 330
+// TFLOP/s, where the exponentials weigh twice as much; 192 and 256 channels, whose
+// accumulators leave one wave a SIMD and nothing to run beside its softmax, 375
+// and 354.
 // The rows of a kv head (its tokens times the heads that share it) are cut into
 // tiles of 32 a wave; a split of the keys, where there are few tiles, leaves
 // sums for kv8_join_kernel.
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
     const int rows = q * a.group, row0 = tile * (32 * WAVES);
     if (q <= 0 || row0 >= rows || c0 < 0 || (int64_t)c0 + q > a.tokens)
         return;
-    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fffffc0)), 0);
+    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fff0000)), 0);
     const int n_pos = a.lens[b];   // positions go by the sequence's own length
 
     // what the workgroup's rows see, and this wave's
@@ -119,31 +121,33 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
             id = table[tok >> bshift];
         return (unsigned)id < (unsigned)a.blocks ? id : -1;
     };
-    int vid_next[NP];
+    // the blocks of the step to come, a step before its codes: a table entry's
+    // trip from memory is not waited for
+    int kid[NP], vid = -1, vid_now = -1;   // V: the thread's pieces share their 16 tokens
+    const auto blocks = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            kid[i] = block_at((s * STEP + (i * THREADS + (int)threadIdx.x) % PIECES / (D / 16)) & ~15);
+        vid = block_at(s * STEP + ((int)threadIdx.x & 3) * 16);
+    };
     const auto fetch = [&](int s) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = (i * THREADS + threadIdx.x) % PIECES;
             const int tok = s * STEP + p / (D / 16), d = p % (D / 16) * 16;
-            const int id = max(block_at(tok & ~15), 0);
-            rk[i] = *(const u32x4 *)(a.ck + ((int64_t)id * a.kv_heads + head) * unit_bytes +
+            rk[i] = *(const u32x4 *)(a.ck + ((int64_t)max(kid[i], 0) * a.kv_heads + head) * unit_bytes +
                                      (int64_t)(tok & (a.bs - 1)) * D + d);
         }
+        vid_now = vid;
+        const int64_t u = (int64_t)max(vid, 0) * a.kv_heads + head;
+        const int vtok = s * STEP + ((int)threadIdx.x & 3) * 16;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int p = (i * THREADS + threadIdx.x) % PIECES;
-            const int tok = s * STEP + (p & 3) * 16, d = p >> 2;
-            vid_next[i] = block_at(tok);
-            rv[i] = *(const u32x4 *)(a.cv + ((int64_t)max(vid_next[i], 0) * a.kv_heads + head) * unit_bytes +
-                                     (int64_t)d * a.bs + (tok & (a.bs - 1)));
+            const int d = (i * THREADS + (int)threadIdx.x) % PIECES >> 2;
+            rv[i] = *(const u32x4 *)(a.cv + u * unit_bytes + (int64_t)d * a.bs + (vtok & (a.bs - 1)));
         }
-        // every thread, for its own 16 tokens of V (threads 0..3 write them)
-        r_sk = r_sv = 0.0f;
-        if (vid_next[0] >= 0) {
-            const int64_t u = (int64_t)vid_next[0] * a.kv_heads + head;
-            r_sk = a.sk[u] * a.scale2;
-            r_sv = a.sv[u];
-        }
+        r_sk = a.sk[u];
+        r_sv = a.sv[u];
     };
     const auto put = [&](int s, int buf) {
         if (PIECES < THREADS && threadIdx.x >= PIECES)
@@ -157,6 +161,9 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
             lk[buf][k_chunk<CH>(tok, c)] = u32x4{w0[0], w0[1], w1[0], w1[1]};
             lk[buf][k_chunk<CH>(tok, c + 1)] = u32x4{w2[0], w2[1], w3[0], w3[1]};
         }
+        // (a scale of a block that is not there may be anything)
+        r_sk = vid_now >= 0 ? r_sk * a.scale2 : 0.0f;
+        r_sv = vid_now >= 0 ? r_sv : 0.0f;
         // V codes that no row sees (0 * NaN), or whose scale is zero, are cleared
         const int vtok = s * STEP + (threadIdx.x & 3) * 16;   // the same for every piece of the thread
         if (!(r_sv > 0.0f) || vtok < lo_all || vtok + 16 > hi_all) {
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
             ls[buf][threadIdx.x][0] = r_sk;
             ls[buf][threadIdx.x][1] = v.log2;
             ls[buf][threadIdx.x][2] = v.inv;
-            ls[buf][threadIdx.x][3] = vid_next[0] >= 0 ? 1.0f : 0.0f;
+            ls[buf][threadIdx.x][3] = vid_now >= 0 ? 1.0f : 0.0f;
         }
     };
 
@@ -200,15 +207,19 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
     bool seen = false;             // the row has seen a key: zero is its reference
 
     if (s0 < s1) {
+        blocks(s0);
         fetch(s0);
+        blocks(s0 + 1);
         put(s0, 0);
     }
     __syncthreads();
     const int krow = ((n >> 2) & 1) * 16 + (n >> 3) * 4 + (n & 3);   // the token in product row n
     for (int s = s0; s < s1; ++s) {
         const int buf = (s - s0) & 1, base = s * STEP;
-        if (s + 1 < s1)
+        if (s + 1 < s1) {
             fetch(s + 1);
+            blocks(s + 2);
+        }
         if (base < w_hi && base + STEP > w_lo) {
             f32x16 sc[2];
 #pragma unroll
@@ -343,7 +354,7 @@ hipError_t launch_waves(const Kv8Attn &a, hipStream_t s)
 int kv8_tile_occupancy(int dc, int waves)
 {
     // eight waves, a step's codes shared by 256 rows: D = 128 (4096 tokens over
-    // 8192: 512 us against 541 with four; D = 64: 104 against 75, 5 prompts of
+    // 8192: 512 us against 541 with four, when that was measured; D = 64: 104 against 75, 5 prompts of
     // up to 1777 tokens, where three workgroups of four are resident)
     return waves == 4 || (waves == 8 && dc == 2) ? tile_occupancy(dc, waves) : 0;
 }
