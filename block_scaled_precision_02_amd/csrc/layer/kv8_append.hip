@@ -10,7 +10,7 @@
 // latency for single tokens.  One workgroup a block, head and operand: it owns
 // all bytes that its scale governs, so that no scale is seen half updated and
 // no atomics are needed.  On one MI355X: 64 single tokens of 8 heads of 128
-// 5.3 us; six prompts, 19002 tokens in all, 38 us, 3.1 TB/s of the bytes they
+// 5.2 us; six prompts, 19002 tokens in all, 36 to 38 us, 3.1 TB/s of the bytes they
 // need: a workgroup's loads, maximum, quotients and stores follow one another,
 // and five workgroups a CU cover for each other only in part (workgroups of 512
 // threads 41 us, registers held to 6 waves a SIMD 58).  Bytes of tokens at or past the sequence's length

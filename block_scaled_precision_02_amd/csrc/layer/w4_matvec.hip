@@ -21,8 +21,8 @@
 // The workgroup's 8 waves split K and meet in LDS; the order of the sums is
 // fixed.
 // On one MI355X, weights not in a cache: 1x21504x5376 int4 in groups of 128 with
-// zero points 17 to 19 us, 3.2 to 3.6 TB/s; 1x8192x8192 MXFP4 13 us; 16x8192x8192
-// MXFP4 19 us, half of it x, which every workgroup lays out for itself.
+// zero points 18 us, 3.4 TB/s; 1x8192x8192 MXFP4 10.7 us, 3.3 TB/s; 16x8192x8192
+// MXFP4 20 us, half of it x, which every workgroup lays out for itself.
 #include <hip/hip_runtime.h>
 
 #include "layer.hpp"
