@@ -25,6 +25,8 @@
 // MXFP4 20 us, half of it x, which every workgroup lays out for itself.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "layer.hpp"
 #include "layer_dev.hpp"
 
@@ -280,25 +282,47 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
 // fetches them 16 bytes a thread, a tile ahead, and takes them from LDS (a byte
 // or two at a time from memory took 6 of 19 us at 1x8192x8192).
 // CPW: chunks a wave and part, at most.
+constexpr int LDS_BYTES = 160 * 1024;   // a workgroup's, at most
+
+// A walk's LDS: the arrays of a fixed size, x, and the tiles' sums that are kept
+// between the parts of a long K (1024 bytes a tile), for which the first two
+// leave room for KEPT tiles a workgroup.
+template <int GROUP, int XR, int CPW, bool ZERO>
+struct WalkLds {
+    static constexpr int W = W4_WAVES, SC = GROUP == 0 ? 4 : CHUNK / GROUP, ESZ = GROUP == 0 ? 1 : 2;
+    static constexpr int RI = XR == 16 ? 4 : XR == 8 ? 2 : 1;   // accumulators that hold rows of x
+    // a tile's scales and zero points: rows of K <= 8192, 16 bytes further apart
+    // where they are whole 16-byte pieces (rows 256 bytes apart are one bank)
+    static constexpr int KC = XR >= 8 ? 64 : W * CPW;           // chunks of a row, at most
+    static constexpr int SB = 16 * (KC * SC * ESZ + 16), ZB = ZERO ? 16 * (KC * SC + 16) : 0;
+    struct Fixed {
+        float red[2][W][16][17];
+        alignas(16) uint8_t tab[2][SB + ZB];
+        alignas(16) float xsum[GROUP == 0 ? 1 : W * CPW][4][SC][RI];   // sums of x, [chunk][lane group]
+    };
+    static constexpr int X = W * CPW * 16 * XR * 16, ROOM = (LDS_BYTES - X - (int)sizeof(Fixed)) / 1024;
+    static constexpr int KEPT = ROOM < 8 ? ROOM : 8;
+    static_assert(KEPT >= 1 && X + (int)sizeof(Fixed) + 1024 * KEPT <= LDS_BYTES, "a workgroup's LDS");
+};
+
 template <int GROUP, int XR, int CPW, bool ZERO>
 __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel(W4Args a)
 {
+    using Lds = WalkLds<GROUP, XR, CPW, ZERO>;
     constexpr int W = W4_WAVES;
     constexpr bool MX = GROUP == 0;
     constexpr bool SWAP = GROUP == 32 || GROUP == 64;
-    constexpr int RI = XR == 16 ? 4 : XR == 8 ? 2 : 1;   // accumulators that hold rows of x
-    constexpr int SC = MX ? 4 : CHUNK / GROUP;           // scales of a chunk
+    constexpr int RI = Lds::RI;
+    constexpr int SC = Lds::SC;                          // scales of a chunk
     constexpr int PG = 4 / SC;                           // products of a scale
-    constexpr int ESZ = MX ? 1 : 2;                      // bytes of a scale
-    // a tile's scales and zero points: rows of K <= 8192, 16 bytes further apart
-    // where they are whole 16-byte pieces (rows 256 bytes apart are one bank)
-    constexpr int KC = XR >= 8 ? 64 : W * CPW;           // chunks of a row, at most
-    constexpr int SB = 16 * (KC * SC * ESZ + 16), ZB = ZERO ? 16 * (KC * SC + 16) : 0;
+    constexpr int ESZ = Lds::ESZ;                        // bytes of a scale
+    constexpr int SB = Lds::SB;
     constexpr int NX = (CPW * XR + 3) / 4;               // 16-byte pieces of x a thread lays out
     extern __shared__ u32x4 xl[];                        // [chunk][product][lane group][XR], then the tiles' sums
-    __shared__ float red[2][W][16][17];
-    __shared__ alignas(16) uint8_t tab[2][SB + ZB];
-    __shared__ alignas(16) float xsum[MX ? 1 : W * CPW][4][SC][RI];   // sums of x, [chunk][lane group]
+    __shared__ typename Lds::Fixed fixed;
+    auto &red = fixed.red;
+    auto &tab = fixed.tab;
+    [[maybe_unused]] auto &xsum = fixed.xsum;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int chunks = (a.K + CHUNK - 1) / CHUNK, groups = a.K / (MX ? 32 : GROUP);
@@ -520,29 +544,32 @@ hipError_t launch_wide(const W4Args &a, hipStream_t s)
     return launch_tiles<GROUP, MT, RI, 1>(a, s);
 }
 
+template <int GROUP, int XR, int CPW, bool ZERO>
+hipError_t launch_zeros(const W4Args &a, hipStream_t s)
+{
+    using Lds = WalkLds<GROUP, XR, CPW, ZERO>;
+    constexpr int NUM_CU = 256;
+    const int tiles = (a.N + 15) / 16, chunks = (a.K + CHUNK - 1) / CHUNK;
+    // as many workgroups as are resident: two a CU while LDS has room for both
+    // (4x8192x8192, 64 KB of x: one 14 us, two 18; 1x21504x5376: 20 and 18)
+    int wgs = Lds::X <= 32768 && XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
+    if (chunks > W4_WAVES * CPW) {   // K in parts: no more tiles a workgroup than have room for their sums
+        wgs = std::max(wgs, (tiles + Lds::KEPT - 1) / Lds::KEPT);
+        kept = (tiles + wgs - 1) / wgs;
+    }
+    hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, ZERO>), dim3((unsigned)std::min(tiles, wgs)),
+                       dim3(W4_WAVES * 64), Lds::X + kept * 1024, s, a);
+    return hipGetLastError();
+}
+
 template <int GROUP, int XR, int CPW>
 hipError_t launch_cpw(const W4Args &a, hipStream_t s)
 {
-    constexpr int NUM_CU = 256, KEPT = 8;   // tiles whose sums are kept, at most
-    const int tiles = (a.N + 15) / 16, chunks = (a.K + CHUNK - 1) / CHUNK;
-    const size_t x_bytes = (size_t)W4_WAVES * CPW * 16 * XR * 16;
-    // as many workgroups as are resident: two a CU while LDS has room for both
-    // (4x8192x8192, 64 KB of x: one 14 us, two 18; 1x21504x5376: 20 and 18)
-    int wgs = x_bytes <= 32768 && XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
-    if (chunks > W4_WAVES * CPW) {
-        wgs = wgs > (tiles + KEPT - 1) / KEPT ? wgs : (tiles + KEPT - 1) / KEPT;
-        kept = (tiles + wgs - 1) / wgs;
-    }
-    const dim3 grid((unsigned)(tiles < wgs ? tiles : wgs)), block(W4_WAVES * 64);
-    const size_t lds = x_bytes + kept * 1024;
     if constexpr (GROUP != 0) {
-        if (a.Z) {
-            hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, true>), grid, block, lds, s, a);
-            return hipGetLastError();
-        }
+        if (a.Z)
+            return launch_zeros<GROUP, XR, CPW, true>(a, s);
     }
-    hipLaunchKernelGGL((w4_walk_kernel<GROUP, XR, CPW, false>), grid, block, lds, s, a);
-    return hipGetLastError();
+    return launch_zeros<GROUP, XR, CPW, false>(a, s);
 }
 
 template <int GROUP, int XR>

@@ -1,0 +1,80 @@
+"""GPU tests of the 4-bit matvec by equality: x, weights and scales are small
+whole numbers and powers of two, so that every sum is exact in binary32 in any
+order and the result is the exact one rounded once to bf16."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import block_scaled_precision_02_amd as q  # noqa: E402
+
+E2M1 = (0, .5, 1, 1.5, 2, 3, 4, 6, -0.0, -.5, -1, -1.5, -2, -3, -4, -6)
+
+
+@pytest.fixture(autouse=True)
+def _gpu_only():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def make(kind, M, N, K, group, seed, zeros=False, bias=False, srows=1):
+    """|x| <= 8, |w - z| <= 15, e2m1 in halves, scales 1/2, 1 or 2: sums stay
+    below 2^24 units of the smallest product up to K = 2^24 / (8 * 15 * 4)."""
+    assert K * 8 * 15 * 4 < 1 << 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def ints(lo, hi, *shape, dtype=torch.float32):
+        return torch.randint(lo, hi, shape, device="cuda", generator=g).to(dtype)
+    d = {"x": ints(-8, 9, M, K).bfloat16(), "w": ints(0, 256, N, K // 2, dtype=torch.uint8), "zeros": None,
+         "bias": ints(-99, 100, N).bfloat16() if bias else None}
+    if kind == "mx":
+        d["scales"] = ints(126, 129, -(-N // srows), K // 32, dtype=torch.uint8)
+    else:
+        d["scales"] = torch.exp2(ints(-1, 2, N, K // group)).bfloat16()
+        if zeros:
+            d["zeros"] = ints(0, 16, N, K // group, dtype=torch.uint8)
+    return d
+
+
+def want(kind, d, group, srows=1):
+    x, N = d["x"].double(), d["w"].shape[0]
+    K = x.shape[1]
+    out = torch.empty(x.shape[0], N, dtype=torch.float64, device="cuda")
+    table = torch.tensor(E2M1, dtype=torch.float64, device="cuda")
+    for n in range(0, N, 8192):                     # in parts: the weights in 64 bits are 16 times their size
+        w = d["w"][n:n + 8192]
+        nib = torch.stack((w & 15, w >> 4), 2).view(-1, K // group, group)
+        if kind == "mx":
+            rows = torch.arange(n, min(n + 8192, N), device="cuda") // srows
+            v = table[nib.int()] * torch.exp2(d["scales"][rows].double() - 127)[..., None]
+        else:
+            z = 8.0 if d["zeros"] is None else d["zeros"][n:n + 8192].double()[..., None]
+            v = (nib.double() - z) * d["scales"][n:n + 8192].double()[..., None]
+        out[:, n:n + 8192] = torch.matmul(x, v.view(-1, K).t())
+    return out if d["bias"] is None else out + d["bias"].double()
+
+
+def run(kind, d, srows=1):
+    if kind == "mx":
+        return q.qgemm_w4_matvec_mx(d["x"], d["w"], d["scales"], srows, bias=d["bias"])
+    return q.qgemm_w4_matvec_i4(d["x"], d["w"], d["scales"], d["zeros"], bias=d["bias"])
+
+
+def check(kind, d, group=32, srows=1):
+    got, exact = run(kind, d, srows), want(kind, d, group, srows)
+    assert exact.abs().max() < 1 << 22                  # in units of 1/4: exact in binary32
+    assert torch.equal(got, exact.to(torch.bfloat16)), torch.nonzero(got != exact.to(torch.bfloat16))[:4]
+
+
+@pytest.mark.parametrize("M", [9, 16])
+@pytest.mark.parametrize("N,K", [(24576, 8192), (24577, 8192), (32768, 8192), (30000, 4224), (128256, 8192)])
+def test_many_tiles_of_a_row_in_parts(M, N, K):
+    """x of more than eight rows and K > 4096 goes in parts; the sums of 7 and
+    more tiles a workgroup, kept between them, do not all find room in LDS."""
+    check("mx", make("mx", M, N, K, 32, N + M))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_many_tiles_of_a_row_in_parts_int4(zeros):
+    check("i4", make("i4", 16, 32769, 8192, 32, 3, zeros), 32)
