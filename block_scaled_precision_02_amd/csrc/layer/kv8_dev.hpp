@@ -101,6 +101,10 @@ __device__ __forceinline__ VScale v_scale(float s, float &held)
 // The weights enter the second product as binary16 between 0 and 2^15.
 constexpr float W_TOP = 15.0f;
 
+// What a row's accumulators are multiplied by: 1 / the sum of its weights, 0
+// where it has seen nothing.  A sum that is not a number (a query's NaN) stays one.
+__device__ __forceinline__ float row_factor(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+
 // The keys that a sequence's new token t (of q, the cache holding n tokens
 // with them) sees: [lo, hi).
 struct Span {

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
             const int64_t tok = c0 + row / a.group;
             const int hq = head * a.group + row % a.group;
             if (a.splits == 1) {
-                const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+                const float inv = row_factor(all);
                 *(u32x2 *)(a.O + tok * a.ldo + hq * D + d) =
                     u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
             } else {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
     }
     uint16_t *out = a.O + (int64_t)(c0 + t) * a.ldo + hq * D;
     if constexpr (WPR == 1) {
-        const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+        const float inv = row_factor(all);
 #pragma unroll
         for (int i = 0; i < DC; ++i)
             out[lane * DC + i] = (uint16_t)pack_bf16(acc[i] * inv, 0.0f);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
             l += part_l[w];
             v += part_o[w][d];
         }
-        out[d] = (uint16_t)pack_bf16(l > 0.0f ? v / l : 0.0f, 0.0f);
+        out[d] = (uint16_t)pack_bf16(l == 0.0f ? 0.0f : v / l, 0.0f);
     }
 }
 

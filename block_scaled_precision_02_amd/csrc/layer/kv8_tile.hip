@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
     const int64_t tok = c0 + row / a.group;
     const int hq = head * a.group + row % a.group;
     if (a.splits == 1) {
-        const float r = l > 0.0f ? 1.0f / l : 0.0f;
+        const float r = row_factor(l);
         uint16_t *out = a.O + tok * a.ldo + hq * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < DT; ++d)

@@ -430,7 +430,8 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
  *   S[j] = sm_scale * sum_d Q[t,h,d] * K[j,d]      over the visible j:
  *          0 <= j < kv_lens[b]; causal: j <= P; window > 0: j > P - window
  *   O[t,h,:] = bf16( sum_j softmax(S)[j] * V[j,:] )
- * A row that sees nothing gives zeros.  Products take Q and the codes
+ * A row that sees nothing gives zeros; a NaN in a row of Q gives NaN in that
+ * row alone.  Products take Q and the codes
  * exactly and the probabilities, times the block's V scale and relative to the
  * row's largest, in binary16; maxima, sums and accumulators are binary32.  V
  * scales below 2^-100 are read as 2^-100, zero as zero.  The result of a call does not depend on timing.

@@ -1,0 +1,60 @@
+"""GPU tests of the 8-bit cache with what is not a number: it comes out where
+it went in, whatever kernel and number of splits the lengths lead to, and
+nowhere else."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import block_scaled_precision_02_amd as q  # noqa: E402
+
+from tests.test_gpu_kv8 import Setup  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _gpu_only():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+HEADS, DIM = 8, 128
+
+
+def splits(s, cache):
+    need = q.lib().qgemm_kv8_attention_workspace(cache._ref, s.tokens, len(s.lens), HEADS, s.max_q, s.max_kv, 1, 0)
+    return max(1, need // (s.tokens * HEADS * (DIM + 2) * 4))
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# new tokens, cached tokens with them, the range of splits they lead to: one
+# token unsplit, up to four splits, more; the same with 24 rows; many rows
+SHAPES = [(1, 300, 1, 1), (1, 1500, 2, 4), (1, 9000, 5, 64), (3, 300, 1, 1), (3, 1500, 2, 4), (3, 9000, 5, 64),
+          (50, 300, 1, 1), (50, 3000, 5, 64)]
+
+
+@pytest.mark.parametrize("n_q,n,least,most", SHAPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_row(n_q, n, least, most, bad):
+    s = Setup("e4m3", 1, DIM, 64, [(n_q, n)], seed=n)
+    cache, Q = s.gpu(), s.bf16(s.tokens, HEADS, DIM).cuda()
+    assert least <= splits(s, cache) <= most
+    args = s.seqs() + (s.max_q, s.max_kv)
+    want = q.qgemm_kv8_attention(cache, Q, *args)
+    t = n_q // 2
+    Q[t, 5, 77] = bad
+    got = q.qgemm_kv8_attention(cache, Q, *args)
+    assert bool(got[t, 5].isnan().all())
+    got[t, 5] = want[t, 5]
+    assert same(got, want)
+
+
+def test_query_rows_that_see_nothing():
+    for n_q, n in ((4, 3), (60, 3)):
+        s = Setup("e4m3", 1, DIM, 64, [(n_q, n)], seed=n_q)
+        Q = s.bf16(s.tokens, HEADS, DIM).cuda()
+        Q[:n_q - n] = float("nan")
+        out = q.qgemm_kv8_attention(s.gpu(), Q, *s.seqs(), s.max_q, s.max_kv)
+        assert not bool(out[:n_q - n].any()) and bool(out[n_q - n:].isfinite().all())
