@@ -101,9 +101,24 @@ __device__ __forceinline__ VScale v_scale(float s, float &held)
 // The weights enter the second product as binary16 between 0 and 2^15.
 constexpr float W_TOP = 15.0f;
 
-// What a row's accumulators are multiplied by: 1 / the sum of its weights, 0
-// where it has seen nothing.  A sum that is not a number (a query's NaN) stays one.
-__device__ __forceinline__ float row_factor(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+// A row's sum of weights (up to 2^15) over their V scales is kept in units of
+// 2^19: 2^31 tokens at the smallest scale, 2^-100, add up to 2^127 units, and one
+// at the largest that bf16 values lead to, 2^121, is 2^-125 of them (the tiled
+// kernel's weights may be 2^8 smaller: 16 bits of a subnormal number).
+constexpr float SUM_UNIT = 0x1p-19f;
+
+// A row's result is its accumulators times pre over sum: pre is a power of two
+// that keeps the reciprocal and the products in range, sum infinite where the
+// row has seen nothing (its accumulators are 0 and stay so).  A sum that is not
+// a number (a query's NaN) stays one.
+struct RowSum {
+    float pre, sum;
+};
+__device__ __forceinline__ RowSum row_sum(float units)
+{
+    const float e = units < 1.0f ? 0x1p32f : 0x1p-32f;
+    return RowSum{SUM_UNIT * e, units == 0.0f ? __builtin_inff() : units * e};
+}
 
 // The keys that a sequence's new token t (of q, the cache holding n tokens
 // with them) sees: [lo, hi).

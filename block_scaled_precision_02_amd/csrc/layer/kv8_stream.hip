@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
                 x[i] = __builtin_amdgcn_exp2f(x[i] - zero);
                 sum += x[i];
             }
-            l[t] = fmaf(l[t], fade, sum * sv.inv);
+            l[t] = fmaf(l[t], fade, sum * SUM_UNIT * sv.inv);
             if (!__all(fade == 1.0f)) {
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
@@ -319,9 +319,12 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
             const int64_t tok = c0 + row / a.group;
             const int hq = head * a.group + row % a.group;
             if (a.splits == 1) {
-                const float inv = row_factor(all);
-                *(u32x2 *)(a.O + tok * a.ldo + hq * D + d) =
-                    u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+                const RowSum f = row_sum(all);
+                const float inv = 1.0f / f.sum;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = acc[i] * f.pre * inv;
+                *(u32x2 *)(a.O + tok * a.ldo + hq * D + d) = u32x2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
             } else {
                 const int64_t at = (tok * a.kv_heads * a.group + hq) * a.splits + split;
                 *(f32x4 *)(a.part + at * D + d) = acc;
@@ -367,10 +370,11 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
     }
     uint16_t *out = a.O + (int64_t)(c0 + t) * a.ldo + hq * D;
     if constexpr (WPR == 1) {
-        const float inv = row_factor(all);
+        const RowSum f = row_sum(all);
+        const float inv = 1.0f / f.sum;
 #pragma unroll
         for (int i = 0; i < DC; ++i)
-            out[lane * DC + i] = (uint16_t)pack_bf16(acc[i] * inv, 0.0f);
+            out[lane * DC + i] = (uint16_t)pack_bf16(acc[i] * f.pre * inv, 0.0f);
         return;
     }
 #pragma unroll
@@ -387,7 +391,8 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(Kv8Attn a)
             l += part_l[w];
             v += part_o[w][d];
         }
-        out[d] = (uint16_t)pack_bf16(l == 0.0f ? 0.0f : v / l, 0.0f);
+        const RowSum f = row_sum(l);
+        out[d] = (uint16_t)pack_bf16(v * f.pre / f.sum, 0.0f);
     }
 }
 

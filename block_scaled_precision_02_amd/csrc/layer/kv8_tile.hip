@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
                     y[16 * t + i] = __builtin_amdgcn_exp2f(y[16 * t + i]);
                     sum += y[16 * t + i];
                 }
-                l = fmaf(sum, inv[t], l);
+                l = fmaf(sum * SUM_UNIT, inv[t], l);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     u32x4 w;
@@ -315,14 +315,19 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
     const int64_t tok = c0 + row / a.group;
     const int hq = head * a.group + row % a.group;
     if (a.splits == 1) {
-        const float r = row_factor(l);
+        const RowSum f = row_sum(l);
+        const float inv = 1.0f / f.sum;
         uint16_t *out = a.O + tok * a.ldo + hq * D + 4 * h;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[d][i] = o[d][i] * f.pre * inv;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *(u32x2 *)(out + 32 * d + 8 * i) = u32x2{pack_bf16(o[d][4 * i] * r, o[d][4 * i + 1] * r),
-                                                         pack_bf16(o[d][4 * i + 2] * r, o[d][4 * i + 3] * r)};
+                *(u32x2 *)(out + 32 * d + 8 * i) =
+                    u32x2{pack_bf16(o[d][4 * i], o[d][4 * i + 1]), pack_bf16(o[d][4 * i + 2], o[d][4 * i + 3])};
+        }
     } else {
         const int64_t at = (tok * a.kv_heads * a.group + hq) * a.splits + split;
 #pragma unroll

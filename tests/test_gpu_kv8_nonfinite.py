@@ -1,6 +1,7 @@
 """GPU tests of the 8-bit cache with what is not a number: it comes out where
 it went in, whatever kernel and number of splits the lengths lead to, and
 nowhere else."""
+import numpy as np
 import pytest
 import torch
 
@@ -8,6 +9,7 @@ pytestmark = pytest.mark.gpu
 
 import block_scaled_precision_02_amd as q  # noqa: E402
 
+from tests import kv8_ref  # noqa: E402
 from tests.test_gpu_kv8 import Setup  # noqa: E402
 
 
@@ -58,3 +60,20 @@ def test_query_rows_that_see_nothing():
         Q[:n_q - n] = float("nan")
         out = q.qgemm_kv8_attention(s.gpu(), Q, *s.seqs(), s.max_q, s.max_kv)
         assert not bool(out[:n_q - n].any()) and bool(out[n_q - n:].isfinite().all())
+
+
+@pytest.mark.parametrize("exponent", [-126, -101, -100, -81, -60, 115, 120])
+@pytest.mark.parametrize("n_q,n", [(1, 700), (1, 20000), (50, 20000)])
+def test_v_scales_at_the_ends(exponent, n_q, n):
+    """All keys alike and every V scale tiny (or huge): the sums stay in
+    range; scales below 2^-100 are read as 2^-100."""
+    s = Setup("i8", 1, DIM, 64, [(n_q, n)], seed=n)
+    s.cache["k_scale"].zero_()
+    if exponent == 120:
+        s.cache["v"].bitwise_and_(63)                   # results within bf16
+    s.cache["v_scale"].fill_(2.0 ** exponent)
+    Q = s.bf16(s.tokens, HEADS, DIM)
+    out = q.qgemm_kv8_attention(s.gpu(), Q.cuda(), *s.seqs(), s.max_q, s.max_kv).float().cpu()
+    s.cache["v_scale"].fill_(2.0 ** max(exponent, -100))
+    want, tol = kv8_ref.attention(s.cache, Q, s.table.tolist(), s.cu, s.lens, "i8")
+    assert (np.abs(out.double().numpy() - want) <= tol).all()
