@@ -1,7 +1,7 @@
 // w4_matvec.hip -- a few rows of bf16 activations times 4-bit weights with
 // group scales, the projections of a decode step.
 //
-//   i4:  y[m,n] = sum_G s[n,G] ( sum_{k in G} x[m,k] w[n,k] - z[n,G] sum_{k in G} x[m,k] ) (+ bias[n])
+//   i4:  y[m,n] = sum_G s[n,G] sum_{k in G} x[m,k] (w[n,k] - z[n,G]) (+ bias[n])
 //   mx:  y[m,n] = sum_k x[m,k] e2m1(w[n,k]) 2^(s[n,k/32] - 127) (+ bias[n])
 //
 // Bound by memory: half a byte a weight and its scales.  The weights go from
@@ -9,10 +9,15 @@
 // sums also for one row of x, because the vector units are busy enough turning
 // 4-bit codes into bf16 (both exact):
 //  * e2m1: the conversion instruction takes the scale along (a power of two).
-//  * int4: a nibble OR-ed into the mantissa of 128 is the bf16 value 128 + w,
-//    two a bit operation (nibbles j and j + 4 of a dword; x is taken in the
-//    same order).  The 128 goes with the zero point: the sum of x over the
-//    group comes from one more product, with ones.
+//  * int4: two masked nibbles of a dword (j and j + 4; x is taken in the same
+//    order) are two subnormal binary16 numbers, which a mixed-precision fused
+//    multiply-add turns into w - z in binary32; its upper half is the bf16
+//    value (|w - z| <= 255 has 8 bits).  The products are the definition's own:
+//    a weight at its zero point adds nothing, an infinite x gives infinities.
+//    (Products with 128 + w, from which 128 + z times the sum of x was taken, need
+//    one operation a weight in place of two, but round 17 times coarser and have
+//    neither: 1x21504x5376 18.4 us in place of 20.4, 16x8192x8192 in groups of 32
+//    26.4 in place of 25.3.)
 // A wave's load is 16 bytes of each of 16 rows and 4 lane groups: 128 weights
 // of a row side by side.  A product sums over 8 elements of every lane group,
 // so that where a scale group is shorter than 128 the dwords are exchanged
@@ -21,7 +26,7 @@
 // The workgroup's 8 waves split K and meet in LDS; the order of the sums is
 // fixed.
 // On one MI355X, weights not in a cache: 1x21504x5376 int4 in groups of 128 with
-// zero points 18 us, 3.4 TB/s; 1x8192x8192 MXFP4 10.7 us, 3.3 TB/s; 16x8192x8192
+// zero points 20.4 us, 3.0 TB/s; 1x8192x8192 MXFP4 10.7 us, 3.3 TB/s; 16x8192x8192
 // MXFP4 20 us, half of it x, which every workgroup lays out for itself.
 #include <hip/hip_runtime.h>
 
@@ -48,20 +53,21 @@ __device__ __forceinline__ u32x4 swap4(u32x4 w)
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight nibbles as 128 + w, in the order 0 4 1 5 2 6 3 7; base: 128 twice, in
-// a vector register (an instruction takes one scalar operand, so that with two
-// constants the and-or would be two).
-__device__ __forceinline__ unsigned nibble_base()
-{
-    unsigned b = 0x43004300u;
-    asm("" : "+v"(b));
-    return b;
-}
-__device__ __forceinline__ bf16x8 nibbles_bf16(unsigned w, unsigned base)
+// Eight nibbles less the zero point, in the order 0 4 1 5 2 6 3 7.  As the
+// mantissa of a binary16 number a nibble w is w 2^-24, or w 2^-20 four bits up.
+__device__ __forceinline__ bf16x8 nibbles_bf16(unsigned w, float z)
 {
     constexpr unsigned M = 0x000f000fu;
-    return __builtin_bit_cast(
-        bf16x8, u32x4{(w & M) | base, ((w >> 4) & M) | base, ((w >> 8) & M) | base, ((w >> 12) & M) | base});
+    const unsigned part[4] = {w & M, w & (M << 4), (w >> 8) & M, (w >> 8) & (M << 4)};
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f16x2 h = __builtin_bit_cast(f16x2, part[i]);
+        const float unit = i & 1 ? 0x1p20f : 0x1p24f;
+        const float lo = fmaf((float)h[0], unit, -z), hi = fmaf((float)h[1], unit, -z);
+        v[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+    }
+    return __builtin_bit_cast(bf16x8, v);
 }
 
 // Eight e2m1 codes times scale (a power of two).
@@ -144,9 +150,6 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             acc[i][t] = f32x4{0, 0, 0, 0};
-    const u32x4 one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
-    [[maybe_unused]] const unsigned base = nibble_base();
 
     for (int cb = c0; cb < c1; cb += U) {
         u32x4 wv[U][NT];
@@ -213,30 +216,29 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
                     const u32x4 v = SWAP ? swap4(wv[u][t]) : wv[u][t];
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        wf[t][p] = nibbles_bf16(v[p], base);
+                        wf[t][p] = nibbles_bf16(v[p], (float)zv[u][t][p / PG]);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
 #pragma unroll
                     for (int j = 0; j < SC; ++j) {
-                        f32x4 xs = {0, 0, 0, 0}, part[NT];
+                        f32x4 part[NT];
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
                             part[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
                         for (int p = j * PG; p < (j + 1) * PG; ++p) {
                             const bf16x8 xf = x_order(xv[i][p]);
-                            xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones, xs, 0, 0, 0);
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
                                 part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, wf[t][p], part[t], 0, 0, 0);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const float s = lo_bf16(sv[u][t][j]), z = 128.0f + (float)(int)zv[u][t][j];
+                            const float s = lo_bf16(sv[u][t][j]);
 #pragma unroll
                             for (int r = 0; r < RI; ++r)
-                                acc[i][t][r] = fmaf(fmaf(-z, xs[r], part[t][r]), s, acc[i][t][r]);
+                                acc[i][t][r] = fmaf(part[t][r], s, acc[i][t][r]);
                         }
                     }
                 }
@@ -273,8 +275,7 @@ __global__ void __launch_bounds__(W4_WAVES * 64) w4_matvec_kernel(W4Args a)
 // The same for up to 16 rows and K up to 8192, the ordinary decode step: a
 // workgroup stays and walks over 16-row tiles of weights.  Wave v's chunks are
 // the same for every tile, so that x (XR rows of it) is laid out once in LDS in
-// the order of the products' operands, and so are its sums over the groups; a
-// product's rows without a row of x repeat others, as nobody reads their sums.
+// the order of the products' operands; a product's rows without a row of x repeat others, as nobody reads their sums.
 // Up to four rows that leaves room for two workgroups a CU.  Where x is too
 // long for LDS, K goes in parts, one walk each, with the tiles' sums kept in
 // LDS between them.  A chunk's register takes the next tile's weights as soon
@@ -298,7 +299,6 @@ struct WalkLds {
     struct Fixed {
         float red[2][W][16][17];
         alignas(16) uint8_t tab[2][SB + ZB];
-        alignas(16) float xsum[GROUP == 0 ? 1 : W * CPW][4][SC][RI];   // sums of x, [chunk][lane group]
     };
     static constexpr int X = W * CPW * 16 * XR * 16, ROOM = (LDS_BYTES - X - (int)sizeof(Fixed)) / 1024;
     static constexpr int KEPT = ROOM < 8 ? ROOM : 8;
@@ -322,7 +322,6 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
     __shared__ typename Lds::Fixed fixed;
     auto &red = fixed.red;
     auto &tab = fixed.tab;
-    [[maybe_unused]] auto &xsum = fixed.xsum;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int chunks = (a.K + CHUNK - 1) / CHUNK, groups = a.K / (MX ? 32 : GROUP);
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
         }
     };
     const auto weights = [&](int tile) { return a.W + (int64_t)min(tile * 16 + r16, a.N - 1) * a.ldw + 16 * g; };
-    [[maybe_unused]] const unsigned base = nibble_base();
     // the row of x that stands in a product's row
     const int xslot = XR == 1 ? 0 : XR == 4 ? r16 >> 2 : XR == 8 ? (r16 >> 2) + 4 * (r16 & 1) : (r16 >> 2) + 4 * (r16 & 3);
 
@@ -420,24 +418,6 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
         }
         stage(blockIdx.x, tab[0]);
         __syncthreads();
-        if constexpr (!MX) {
-            // sums of x over the groups: products with ones, whose columns are all alike
-            const u32x4 one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-            const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
-            for (int c = 0; c < nc; ++c)
-#pragma unroll
-                for (int j = 0; j < SC; ++j) {
-                    f32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-                    for (int p = j * PG; p < (j + 1) * PG; ++p)
-                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(c, p), ones, sum, 0, 0, 0);
-                    if (r16 == 0)
-#pragma unroll
-                        for (int r = 0; r < RI; ++r)
-                            xsum[l0 + c][g][j][r] = sum[r];   // read by this wave alone
-                }
-        }
-
         // A tile: its sums, with the next one's loads; the next one's scales to
         // LDS; one barrier (a buffer's last readers have passed the barrier of
         // the tile between); the result.
@@ -447,8 +427,8 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
             const bool more = tile + step < tiles;   // weights past the last tile cost 3 of 14 us at 1x8192x8192, MXFP4
             const uint8_t *w = weights(next), *sz = tab[flip];
             load_scales(next);
-            // x and its sums are the same for every tile: an offset that the
-            // compiler cannot see through keeps them in LDS and out of the registers
+            // x is the same for every tile: an offset that the compiler cannot see
+            // through keeps it in LDS and out of the registers
             int here = 0;
             asm volatile("" : "+s"(here));
             f32x4 acc = {0, 0, 0, 0};
@@ -485,16 +465,16 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
                         z4 = *(const Zeros *)(zrow + at);
 #pragma unroll
                     for (int j = 0; j < SC; ++j) {
+                        const float z = ZERO ? (float)z4.z[j] : 8.0f;
                         f32x4 part_sum = {0, 0, 0, 0};
 #pragma unroll
                         for (int p = j * PG; p < (j + 1) * PG; ++p)
                             part_sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(c + here, p),
-                                                                               nibbles_bf16(v[p], base), part_sum, 0, 0, 0);
+                                                                               nibbles_bf16(v[p], z), part_sum, 0, 0, 0);
                         const float s = __uint_as_float((unsigned)s4.s[j] << 16);
-                        const float z = ZERO ? 128.0f + (float)z4.z[j] : 136.0f;
 #pragma unroll
                         for (int r = 0; r < RI; ++r)
-                            acc[r] = fmaf(fmaf(-z, xsum[l0 + c + here][g][j][r], part_sum[r]), s, acc[r]);
+                            acc[r] = fmaf(part_sum[r], s, acc[r]);
                     }
                 }
             }

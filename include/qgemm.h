@@ -472,7 +472,9 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
  *   elements, [N, K/32] or [ceil(N/32), K/32] by b_layout); the activations
  *   stay bf16.  Scale code 255 is NaN; an element times its scale has to lie
  *   within bf16.
- * Weights and X enter the products exactly, sums are binary32 in an order
+ * Weights (int4: w - zero) and X enter the products exactly, so that a weight at
+ * its zero point adds nothing and an infinite X gives what the formula does;
+ * sums are binary32 in an order
  * that depends on the shape alone.  Any N; K a positive multiple of the group
  * (mx: 32). */
 qgemm_status qgemm_w4_matvec_i4(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw,

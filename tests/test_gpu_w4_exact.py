@@ -78,3 +78,66 @@ def test_many_tiles_of_a_row_in_parts(M, N, K):
 @pytest.mark.parametrize("zeros", [False, True])
 def test_many_tiles_of_a_row_in_parts_int4(zeros):
     check("i4", make("i4", 16, 32769, 8192, 32, 3, zeros), 32)
+
+
+SHAPES = [(1, 50, 2048), (4, 50, 2048), (8, 50, 2048), (16, 50, 8192), (2, 40, 384), (17, 40, 384), (64, 8200, 384)]
+
+
+def real(M, N, K, group, seed):
+    d = make("i4", M, N, K, group, seed, True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 1)
+    d["x"] = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    return d
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("z", [0, 8, 15, None])
+def test_weights_at_their_zero_point_add_nothing(M, N, K, group, z):
+    d = real(M, N, K, group, M)
+    if z is None:                                        # 8 where there are no zero points
+        d["zeros"], z = None, 8
+    else:
+        d["zeros"][:7] = z
+    d["w"][:7] = 17 * z
+    d["x"][0] *= 2.0 ** 100
+    out = run("i4", d)
+    assert not bool(out[:, :7].any()) and bool((out[:, 7:] != 0).any())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_an_infinite_x(M, N, K, group):
+    """Infinity times w - z: its sign, and NaN where they are equal; other rows
+    keep their bits."""
+    d = real(M, N, K, group, M)
+    before = run("i4", d)
+    row, k = M // 2, K - 3
+    d["x"][row, k] = float("-inf")
+    out = run("i4", d)
+    diff = (d["w"][:, k // 2] >> 4 if k & 1 else d["w"][:, k // 2] & 15).float() - d["zeros"][:, k // group].float()
+    exact = torch.where(diff == 0, float("nan"), diff * float("-inf"))
+    assert torch.equal(out[row].isnan(), exact.isnan()) and torch.equal(out[row].nan_to_num(), exact.bfloat16().nan_to_num())
+    keep = torch.arange(M, device="cuda") != row
+    assert torch.equal(out[keep], before[keep])
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_sums_near_the_top_of_the_range(M, N, K, group):
+    d = real(M, N, K, group, M)
+    d["x"][:] = 2.0 ** 113
+    d["w"][:] = 0x99
+    d["zeros"][:] = 8
+    d["scales"][:] = 1.0
+    assert torch.equal(run("i4", d), torch.full((M, N), K * 2.0 ** 113, device="cuda").bfloat16())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_zero_points_of_eight_bits(M, N, K, group):
+    d = make("i4", M, N, K, group, 7, True)
+    d["zeros"] = torch.randint(0, 256, d["zeros"].shape, device="cuda", dtype=torch.uint8)
+    d["x"] = d["x"].sign()
+    check("i4", d, group)
