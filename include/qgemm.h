@@ -474,8 +474,9 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
  *   within bf16.
  * Weights (int4: w - zero) and X enter the products exactly, so that a weight at
  * its zero point adds nothing and an infinite X gives what the formula does;
- * sums are binary32 in an order
- * that depends on the shape alone.  Any N; K a positive multiple of the group
+ * sums are binary32 in an order that depends on the shape, the kind and layout
+ * of the scales, and on whether the scales and zeros are 16-byte aligned, alone
+ * (aligned ones are read faster).  Any N; K a positive multiple of the group
  * (mx: 32). */
 qgemm_status qgemm_w4_matvec_i4(const uint16_t *X, int64_t ldx, const uint8_t *W, int64_t ldw,
                                 const uint16_t *scales, const uint8_t *zeros, int64_t group, const uint16_t *bias,

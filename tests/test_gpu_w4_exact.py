@@ -141,3 +141,16 @@ def test_zero_points_of_eight_bits(M, N, K, group):
     d["zeros"] = torch.randint(0, 256, d["zeros"].shape, device="cuda", dtype=torch.uint8)
     d["x"] = d["x"].sign()
     check("i4", d, group)
+
+
+@pytest.mark.parametrize("kind,group", [("i4", 32), ("i4", 128), ("mx", 32)])
+@pytest.mark.parametrize("M", [1, 16])
+def test_tables_that_are_not_16_byte_aligned(kind, group, M):
+    d = make(kind, M, 200, 2048, group, 5, kind == "i4")
+    for n in ("scales", "zeros"):
+        if d[n] is not None:
+            buf = torch.empty(d[n].numel() + 1, dtype=d[n].dtype, device="cuda")
+            buf[1:] = d[n].view(-1)
+            d[n] = buf[1:].view(d[n].shape)
+            assert d[n].data_ptr() % 16
+    check(kind, d, group)
