@@ -71,12 +71,16 @@ __device__ __forceinline__ void times_gamma(Piece &h, const u32x4 *g, int p)
     }
 }
 
+// The larger one, NaN where either is: what is not a number in a row shows in
+// its scale.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ float max_abs(const Piece &h)
 {
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fabsf(h.v[i]));
+        m = max_nan(m, fabsf(h.v[i]));
     return m;
 }
 
@@ -113,7 +117,7 @@ __device__ __forceinline__ void emit(Piece y, float rstd, float row_scale, int p
         float m = live ? max_abs(y) : 0.0f;
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1)
-            m = fmaxf(m, __shfl_xor(m, off));
+            m = max_nan(m, __shfl_xor(m, off));
         const float s = m / 448.0f;
         over_scale(y, s);
         if (live && (p & 15) == 0)
@@ -121,11 +125,11 @@ __device__ __forceinline__ void emit(Piece y, float rstd, float row_scale, int p
     } else {
         constexpr unsigned EMAX = OUT == NORM_MX_E4M3 ? 8u : 2u;
         float m = live ? max_abs(y) : 0.0f;
-        m = fmaxf(m, __shfl_xor(m, 1));
-        m = fmaxf(m, __shfl_xor(m, 2));
+        m = max_nan(m, __shfl_xor(m, 1));
+        m = max_nan(m, __shfl_xor(m, 2));
         const unsigned E = (__float_as_uint(m) >> 23) & 0xffu;
-        const unsigned code = E > EMAX ? E - EMAX : 0u;
-        const float mul = __uint_as_float((254u - code) << 23);   // 2^(127 - code), exact
+        const unsigned code = E == 255u ? 255u : E > EMAX ? E - EMAX : 0u;   // 255: NaN
+        const float mul = __uint_as_float((254u - code) << 23);   // 2^(127 - code), exact (255: any)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             y.v[i] *= mul;
@@ -146,12 +150,12 @@ __device__ __forceinline__ void emit(Piece y, float rstd, float row_scale, int p
 }
 
 // 1/sqrt(v), v >= 0, to half a unit in the last place (0 for 0: a zero row
-// with eps 0 stays zero).  One Newton step on the hardware's estimate r,
+// with eps 0 stays zero; NaN for NaN).  One Newton step on the hardware's estimate r,
 // r + r (1 - v r^2) / 2, with the residual formed exactly: v r = t + u.
 __device__ __forceinline__ float inv_sqrt(float v)
 {
     if (!(v > 1e-30f && v < 1e30f))
-        return v > 0.0f ? 1.0f / __builtin_sqrtf(v) : 0.0f;
+        return v == 0.0f ? 0.0f : 1.0f / __builtin_sqrtf(v);
     const float r = __builtin_amdgcn_rsqf(v);
     const float t = v * r, u = fmaf(v, r, -t);
     const float e = fmaf(-u, r, fmaf(-t, r, 1.0f));
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(NormArgs a)
                 store_h(o, p, keep[c]);
             times_gamma(keep[c], g, p);
         }
-        top = fmaxf(top, max_abs(keep[c]));
+        top = max_nan(top, max_abs(keep[c]));
     }
     for (int p = t + THREADS * KEEP; p < np; p += THREADS) {
         Piece h = load_h<RES>(x, r, p);
@@ -199,12 +203,12 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(NormArgs a)
         for (int i = 0; i < 8; ++i)
             sum = fmaf(h.v[i], h.v[i], sum);
         times_gamma(h, g, p);
-        top = fmaxf(top, max_abs(h));
+        top = max_nan(top, max_abs(h));
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
         sum += __shfl_xor(sum, off);
-        top = fmaxf(top, __shfl_xor(top, off));
+        top = max_nan(top, __shfl_xor(top, off));
     }
     if constexpr (WAVES > 1) {
         __shared__ float wsum[WAVES], wtop[WAVES];
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(NormArgs a)
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) {
             sum += wsum[w];
-            top = fmaxf(top, wtop[w]);
+            top = max_nan(top, wtop[w]);
         }
     }
     const float rstd = inv_sqrt(sum / (float)a.K + a.eps);

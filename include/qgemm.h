@@ -354,8 +354,11 @@ qgemm_status qgemm_quant_f8_block(const uint16_t *X, int64_t ldx, uint8_t *Q, in
  *   scale  [M] fp32;  S [M, K/128] fp32 or [M, K/32] bytes, row stride lds
  *          elements
  * X, R, gamma, Rout, Q 16-byte aligned; fp32 scales 4-byte; K a positive
- * multiple of 32 (f8_block: 128).  M == 0 is a no-op.  Inputs are finite: a
- * row holding NaN or infinity gets unspecified codes and scales. */
+ * multiple of 32 (f8_block: 128).  M == 0 is a no-op.  What is not finite shows
+ * in the scales, and so in the GEMM's row: a row of h * gamma that holds NaN has
+ * NaN scales (MX: code 255), one that holds an infinity in its own block at
+ * least; the codes under a NaN scale are unspecified.  Rows whose sum of h^2
+ * passes binary32 give zeros, as the formula in binary32 does. */
 qgemm_status qgemm_rmsnorm_quant_i8_rowwise(const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
                                             const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo,
                                             int8_t *Q, int64_t ldq, float *scale, int64_t M, int64_t K,
