@@ -450,7 +450,8 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
  * Positions whose block-table entry lies outside [0, num_blocks) or past width
  * count as not visible.  Nothing of a block is read past the rows' visible
  * range that could reach the result: bytes there may hold anything, NaN codes
- * included; visible codes are finite, visible scales finite and >= 0. */
+ * included; visible codes are finite, visible scales finite and >= 0, or NaN: a
+ * row that sees a token of a block whose K or V scale is NaN becomes NaN. */
 int64_t qgemm_kv8_attention_workspace(const qgemm_kv8_cache *cache, int64_t tokens, int64_t batch, int64_t heads,
                                       int64_t max_q, int64_t max_kv, int causal, int64_t window);
 qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q, int64_t ldq,

@@ -77,3 +77,27 @@ def test_v_scales_at_the_ends(exponent, n_q, n):
     s.cache["v_scale"].fill_(2.0 ** max(exponent, -100))
     want, tol = kv8_ref.attention(s.cache, Q, s.table.tolist(), s.cu, s.lens, "i8")
     assert (np.abs(out.double().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("n_q,n,window", [(1, 300, 0), (1, 1500, 0), (1, 9000, 0), (6, 300, 40), (3, 9000, 0),
+                                          (200, 500, 0), (200, 500, 70), (50, 3000, 0), (300, 300, 0)])
+def test_rows_that_see_a_block_without_a_scale(which, fmt, n_q, n, window):
+    s = Setup(fmt, 2, DIM, 32, [(n_q, n), (2, 100)], seed=n)
+    s.cache["v_scale"][s.table[0, 2::3], 1] = 0.0            # blocks whose scale is zero, beside and behind it
+    j = max(0, n - n_q // 2 - 20) // 32
+    s.cache["v_scale"][s.table[0, j], 1] = 0.01
+    Q = s.bf16(s.tokens, HEADS, DIM).cuda()
+    args = s.seqs() + (s.max_q, s.max_kv)
+    want = q.qgemm_kv8_attention(s.gpu(), Q, *args, window=window)
+    s.cache[which][s.table[0, j], 1] = float("nan")
+    got = q.qgemm_kv8_attention(s.gpu(), Q, *args, window=window)
+    at = n - n_q + torch.arange(n_q, device="cuda")          # positions of the first sequence's new tokens
+    sees = at >= 32 * j
+    if window:
+        sees &= at - window < 32 * j + 31
+    rows = torch.nonzero(sees).flatten()
+    assert len(rows) and bool(got[rows, HEADS // 2:].isnan().all())
+    got[rows, HEADS // 2:] = want[rows, HEADS // 2:]
+    assert same(got, want)
