@@ -9,7 +9,8 @@
 // Bound by memory (2 bytes read, 1 written an element) for prompts, by
 // latency for single tokens.  One workgroup a block, head and operand: it owns
 // all bytes that its scale governs, so that no scale is seen half updated and
-// no atomics are needed.  On one MI355X: 64 single tokens of 8 heads of 128
+// no atomics are needed.  A NaN or an infinity among the new values makes the
+// scale NaN, which the maximum hands on to later appends.  On one MI355X: 64 single tokens of 8 heads of 128
 // 5.2 us; six prompts, 19002 tokens in all, 36 to 38 us, 3.1 TB/s of the bytes they
 // need: a workgroup's loads, maximum, quotients and stores follow one another,
 // and five workgroups a CU cover for each other only in part (workgroups of 512
@@ -67,6 +68,9 @@ __device__ __forceinline__ unsigned requantise(unsigned w, float was, const Divi
     codes4_f32<FMT>(w, v);
     return enc4<FMT>(d(v[0] * was), d(v[1] * was), d(v[2] * was), d(v[3] * was));
 }
+
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 // The byte mask of the tokens [lo, hi) among the four from t0 on.
 __device__ __forceinline__ unsigned byte_mask(int t0, int lo, int hi)
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(Kv8Append a)
     const auto widen = [&](u32x4 w) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, fmaxf(fabsf(lo_bf16(w[i])), fabsf(hi_bf16(w[i]))));
+            top = max_nan(top, max_nan(fabsf(lo_bf16(w[i])), fabsf(hi_bf16(w[i]))));
     };
 #pragma unroll
     for (int c = 0; c < AP_KEEP; ++c) {
@@ -144,14 +148,16 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(Kv8Append a)
         widen(piece(p));
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
-        top = fmaxf(top, __shfl_xor(top, off));
+        top = max_nan(top, __shfl_xor(top, off));
     if ((t & 63) == 0)
         wtop[t >> 6] = top;
     __syncthreads();                        // also: every thread has read the scale
 #pragma unroll
     for (int w = 0; w < AP_THREADS / 64; ++w)
-        top = fmaxf(top, wtop[w]);
-    const float now = fmaxf(was, top * (FMT == KV8_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f));
+        top = max_nan(top, wtop[w]);
+    float now = max_nan(was, top * (FMT == KV8_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f));
+    if (!(now < __builtin_inff()))
+        now = __builtin_nanf("");
     const bool grown = old > 0 && now > was;
     const Divider<FMT == KV8_E4M3> div(now);
     if (t == 0)

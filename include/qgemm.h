@@ -421,7 +421,9 @@ typedef struct {
  * their bytes; a scale without older tokens is ignored and overwritten.  A
  * block that several sequences share must not be touched by a call.  Tokens
  * whose position is negative or whose block-table entry lies outside
- * [0, num_blocks) or [0, width) are not stored.  Inputs are finite. */
+ * [0, num_blocks) or [0, width) are not stored.  A block and head whose new
+ * keys (values) hold a NaN or an infinity gets a NaN scale, which stays until the
+ * block is begun anew; its new codes are unspecified. */
 qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, int64_t ldk, const uint16_t *V,
                               int64_t ldv, const int32_t *block_table, int64_t ldt, int64_t width,
                               const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t tokens, int64_t batch,

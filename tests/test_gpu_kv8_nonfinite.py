@@ -79,6 +79,49 @@ def test_v_scales_at_the_ends(exponent, n_q, n):
     assert (np.abs(out.double().numpy() - want) <= tol).all()
 
 
+BAD = [float("nan"), float("inf"), float("-inf")]
+NAMES = ("k", "v", "k_scale", "v_scale")
+
+
+def held(cache):
+    return {n: getattr(cache, n).view(torch.uint8).clone() for n in NAMES}
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("seqs", [[(1, 70), (1, 9)], [(90, 150), (3, 20)]])
+def test_append_shows_it_in_the_scale(fmt, which, bad, seqs):
+    s = Setup(fmt, 3, 64, 32, seqs, seed=4)
+    new = {n: s.bf16(s.tokens, 3, 64).cuda() for n in "kv"}
+    table, cu, lens = s.seqs()
+    good, cache = s.gpu(), s.gpu()
+    q.qgemm_kv8_append(good, new["k"], new["v"], table, cu, lens, s.max_q)
+    new[which][s.cu[1] - 1, 1, 33] = bad                    # the first sequence's last token, head 1
+    q.qgemm_kv8_append(cache, new["k"], new["v"], table, cu, lens, s.max_q)
+    n = s.lens[0]
+    blk = s.table[0, (n - 1) // 32]
+    name = which + "_scale"
+    assert bool(getattr(cache, name)[blk, 1].isnan()) and bool(getattr(good, name)[blk, 1].isfinite())
+    a, b = held(cache), held(good)
+    hit = getattr(cache, which)[blk, 1].view(torch.uint8)
+    past = hit[n % 32:] if which == "k" else hit[:, n % 32:]
+    was = getattr(good, which)[blk, 1].view(torch.uint8)
+    assert torch.equal(past, was[n % 32:] if which == "k" else was[:, n % 32:])
+    for d in (a, b):                                        # everything else keeps its bits
+        d[which][blk, 1] = 0
+        d[name].view(torch.float32)[blk, 1] = 0
+    for x in NAMES:
+        assert torch.equal(a[x], b[x]), x
+    # a finite token more: the scale stays; the block begun anew: it is gone
+    one = torch.ones(1, 3, 64, device="cuda").bfloat16()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q.qgemm_kv8_append(cache, one, one, table[:1], i32(0, 1), i32(n + 1), 1)
+    assert bool(getattr(cache, name)[blk, 1].isnan())
+    q.qgemm_kv8_append(cache, one, one, table[:1], i32(0, 1), i32((n - 1) // 32 * 32 + 1), 1)
+    assert bool(getattr(cache, name)[blk, 1].isfinite())
+
+
 @pytest.mark.parametrize("which", ["k_scale", "v_scale"])
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
 @pytest.mark.parametrize("n_q,n,window", [(1, 300, 0), (1, 1500, 0), (1, 9000, 0), (6, 300, 40), (3, 9000, 0),
