@@ -20,6 +20,8 @@
 // 4.2 us, which is a launch and two trips to memory.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "layer.hpp"
 #include "layer_dev.hpp"
 
@@ -280,15 +282,29 @@ hipError_t launch_out(const NormArgs &a, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_rmsnorm_quant(int out, const NormArgs &a, hipStream_t s)
+hipError_t launch_rmsnorm_quant(int out, const NormArgs &all, hipStream_t s)
 {
-    switch (out) {
-    case NORM_I8_ROW: return launch_out<NORM_I8_ROW>(a, s);
-    case NORM_F8_ROW: return launch_out<NORM_F8_ROW>(a, s);
-    case NORM_F8_BLOCK: return launch_out<NORM_F8_BLOCK>(a, s);
-    case NORM_MX_E4M3: return launch_out<NORM_MX_E4M3>(a, s);
-    default: return launch_out<NORM_MX_E2M1>(a, s);
+    // a launch holds fewer than 2^32 threads: more rows than that go in several
+    constexpr int ROWS = 1 << 23;
+    hipError_t e = hipSuccess;
+    for (int64_t row = 0; row < all.M && e == hipSuccess; row += ROWS) {
+        NormArgs a = all;
+        a.M = (int)std::min<int64_t>(ROWS, all.M - row);
+        a.X += row * a.ldx;
+        a.R = a.R ? a.R + row * a.ldr : nullptr;
+        a.Rout = a.Rout ? a.Rout + row * a.ldo : nullptr;
+        a.Q += row * a.ldq;
+        const int64_t scale = out <= NORM_F8_ROW ? 4 : a.lds * (out == NORM_F8_BLOCK ? 4 : 1);   // bytes a row
+        a.S = (uint8_t *)a.S + row * scale;
+        switch (out) {
+        case NORM_I8_ROW: e = launch_out<NORM_I8_ROW>(a, s); break;
+        case NORM_F8_ROW: e = launch_out<NORM_F8_ROW>(a, s); break;
+        case NORM_F8_BLOCK: e = launch_out<NORM_F8_BLOCK>(a, s); break;
+        case NORM_MX_E4M3: e = launch_out<NORM_MX_E4M3>(a, s); break;
+        default: e = launch_out<NORM_MX_E2M1>(a, s); break;
+        }
     }
+    return e;
 }
 
 }  // namespace qgemm
