@@ -504,11 +504,25 @@ __global__ void __launch_bounds__(W4_WAVES * 64, XR <= 4 ? 4 : 2) w4_walk_kernel
 }
 
 template <int GROUP, int MT, int RI, int NT>
-hipError_t launch_tiles(const W4Args &a, hipStream_t s)
+hipError_t launch_tiles(const W4Args &all, hipStream_t s)
 {
-    hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, NT>), dim3((unsigned)((a.N + 16 * NT - 1) / (16 * NT))),
-                       dim3(W4_WAVES * 64), 0, s, a);
-    return hipGetLastError();
+    // a launch holds fewer than 2^32 threads: more rows of weights than that go
+    // in several (a multiple of 32, an MX scale's rows)
+    constexpr int ROWS = 1 << 26;
+    hipError_t e = hipSuccess;
+    for (int64_t n = 0; n < all.N && e == hipSuccess; n += ROWS) {
+        W4Args a = all;
+        a.N = (int)std::min<int64_t>(ROWS, all.N - n);
+        a.W += n * a.ldw;
+        a.S = (const uint8_t *)a.S + n / a.srows * (a.K / (GROUP ? GROUP : 32)) * (GROUP ? 2 : 1);
+        a.Z = a.Z ? a.Z + n * (a.K / (GROUP ? GROUP : 32)) : nullptr;
+        a.bias = a.bias ? a.bias + n : nullptr;
+        a.Y += n;
+        hipLaunchKernelGGL((w4_matvec_kernel<GROUP, MT, RI, NT>), dim3((unsigned)((a.N + 16 * NT - 1) / (16 * NT))),
+                           dim3(W4_WAVES * 64), 0, s, a);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <int GROUP, int MT, int RI>
