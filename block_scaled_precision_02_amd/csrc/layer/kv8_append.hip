@@ -18,6 +18,8 @@
 // keep what they held.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv8_dev.hpp"
 
 namespace qgemm {
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(Kv8Append a)
     const int start = len - q;
     if (q <= 0 || len <= 0)
         return;
-    const int64_t blk = (int64_t)(max(start, 0) / bs) + blockIdx.x;
+    const int64_t blk = (int64_t)(max(start, 0) / bs) + a.at + blockIdx.x;
     if (blk >= a.width || blk * bs >= len)
         return;
     const int first = (int)(blk * bs);
@@ -257,16 +259,25 @@ hipError_t launch_fmt(const Kv8Append &a, dim3 grid, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_kv8_append(const Kv8Append &a, hipStream_t s)
+hipError_t launch_kv8_append(const Kv8Append &all, hipStream_t s)
 {
-    // q tokens touch at most (q + bs - 2) / bs + 1 blocks, whatever they start at
-    const dim3 grid((unsigned)((a.max_q + a.bs - 2) / a.bs + 1), (unsigned)a.kv_heads * 2, (unsigned)a.batch);
-    switch (a.dim) {
-    case 64: return launch_fmt<64>(a, grid, s);
-    case 128: return launch_fmt<128>(a, grid, s);
-    case 192: return launch_fmt<192>(a, grid, s);
-    default: return launch_fmt<256>(a, grid, s);
+    // q tokens touch at most (q + bs - 2) / bs + 1 blocks, whatever they start at;
+    // a launch holds fewer than 2^32 threads along an axis: more go in several
+    constexpr int64_t BLOCKS = 1 << 23;
+    const int64_t n = ((int64_t)all.max_q + all.bs - 2) / all.bs + 1;
+    hipError_t e = hipSuccess;
+    for (int64_t at = 0; at < n && e == hipSuccess; at += BLOCKS) {
+        Kv8Append a = all;
+        a.at = (int)at;
+        const dim3 grid((unsigned)std::min(BLOCKS, n - at), (unsigned)a.kv_heads * 2, (unsigned)a.batch);
+        switch (a.dim) {
+        case 64: e = launch_fmt<64>(a, grid, s); break;
+        case 128: e = launch_fmt<128>(a, grid, s); break;
+        case 192: e = launch_fmt<192>(a, grid, s); break;
+        default: e = launch_fmt<256>(a, grid, s); break;
+        }
     }
+    return e;
 }
 
 }  // namespace qgemm

@@ -29,6 +29,7 @@ struct Kv8Append {
     const int32_t *table, *cu, *lens; // [batch, ldt], [batch + 1], [batch]
     int64_t ldk, ldv, ldt, tokens;
     int blocks, kv_heads, dim, bs, fmt, width, batch, max_q;
+    int at;                           // the launch's first block of a sequence's new tokens
 };
 hipError_t launch_kv8_append(const Kv8Append &a, hipStream_t s);
 

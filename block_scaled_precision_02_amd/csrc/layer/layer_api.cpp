@@ -227,7 +227,7 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
     TRY(check_device());
     const Kv8Append a = {(uint8_t *)cache->k, (uint8_t *)cache->v, cache->k_scale, cache->v_scale, K, V, block_table,
                          cu_seqlens, kv_lens, ldk, ldv, ldt, tokens, (int)cache->num_blocks, cache->kv_heads,
-                         cache->head_dim, cache->block, cache->fmt, (int)width, (int)batch, (int)max_q};
+                         cache->head_dim, cache->block, cache->fmt, (int)width, (int)batch, (int)max_q, 0};
     return launch([&] { return launch_kv8_append(a, (hipStream_t)stream); });
 }
 

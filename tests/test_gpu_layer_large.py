@@ -49,3 +49,33 @@ def test_matvec_of_many_weight_rows(kind, srows, M):
         part = dict(d, w=d["w"][lo:hi], bias=d["bias"][lo:hi], scales=d["scales"][lo // srows:-(-hi // srows)],
                     zeros=None if d["zeros"] is None else d["zeros"][lo:hi])
         assert torch.equal(got[:, lo:hi], want(kind, part, 32, srows).bfloat16()), lo
+
+
+def test_append_of_many_blocks():
+    """2^28 + 21 new tokens of one sequence, of which a few blocks are held."""
+    import numpy as np
+    from tests import kv8_ref
+    bs, dim, n = 16, 64, (1 << 28) + 21
+    width = -(-n // bs)
+    places = [0, (1 << 23) - 1, 1 << 23, (1 << 24) - 1, 1 << 24, width - 1]
+    x = torch.zeros(n, 1, dim, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    cache = q.KV8Cache.empty(len(places), 1, dim, bs)
+    rng = np.random.default_rng(1)
+    rows = {}
+    for i, p in enumerate(places):
+        m = min(bs, n - p * bs)
+        rows[i] = torch.from_numpy(rng.standard_normal((m, 1, dim)).astype(np.float32)).bfloat16()
+        x[p * bs:p * bs + m] = rows[i].cuda()
+        table[0, p] = i
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q.qgemm_kv8_append(cache, x, x, table, i32(0, n), i32(n), n)
+    for i, row in rows.items():
+        m = row.shape[0]
+        ref = {"k": torch.zeros(1, 1, bs, dim, dtype=torch.float8_e4m3fn),
+               "v": torch.zeros(1, 1, dim, bs, dtype=torch.float8_e4m3fn), "k_scale": torch.zeros(1, 1),
+               "v_scale": torch.zeros(1, 1)}
+        kv8_ref.append(ref, row, row, [[0]], [0, m], [m], "e4m3")
+        assert torch.equal(bits(cache.k[i, :, :m]).cpu(), bits(ref["k"][0, :, :m])), places[i]
+        assert torch.equal(bits(cache.v[i, :, :, :m]).cpu(), bits(ref["v"][0, :, :, :m])), places[i]
+        assert torch.equal(cache.k_scale[i].cpu(), ref["k_scale"][0]) and torch.equal(cache.v_scale[i].cpu(), ref["v_scale"][0])
