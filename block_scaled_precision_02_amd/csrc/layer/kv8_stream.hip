@@ -81,10 +81,10 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
     const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
     const int head = blockIdx.y, b = blockIdx.z;
     const int c0 = a.cu[b], q = a.cu[b + 1] - c0;
-    const int rows = q * a.group, row0 = tile * (16 * NT);
+    const int rows = min(q, a.max_q) * a.group, row0 = tile * (16 * NT);
     if (q <= 0 || row0 >= rows || c0 < 0 || (int64_t)c0 + q > a.tokens)
         return;
-    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fff0000)), 0);
+    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)min(a.max_kv, 0x7fff0000))), 0);
     const int qlen_pos = a.lens[b];   // positions go by the sequence's own length
 
     // the tile's rows and what they see

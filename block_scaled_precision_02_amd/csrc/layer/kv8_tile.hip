@@ -80,10 +80,10 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
     const int head = blockIdx.x, b = blockIdx.z;
     const int split = blockIdx.y % a.splits, tile = a.row_tiles - 1 - blockIdx.y / a.splits;   // longest first
     const int c0 = a.cu[b], q = a.cu[b + 1] - c0;
-    const int rows = q * a.group, row0 = tile * (32 * WAVES);
+    const int rows = min(q, a.max_q) * a.group, row0 = tile * (32 * WAVES);
     if (q <= 0 || row0 >= rows || c0 < 0 || (int64_t)c0 + q > a.tokens)
         return;
-    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)0x7fff0000)), 0);
+    const int len = max(min(a.lens[b], (int)min((int64_t)a.width * a.bs, (int64_t)min(a.max_kv, 0x7fff0000))), 0);
     const int n_pos = a.lens[b];   // positions go by the sequence's own length
 
     // what the workgroup's rows see, and this wave's

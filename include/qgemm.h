@@ -444,7 +444,8 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
  *                elements (multiples of 8), heads adjacent, 16-byte aligned
  *   block_table, cu_seqlens, kv_lens   as for the append
  *   max_q, max_kv   at least the largest count of new tokens and the largest
- *                kv_lens: tokens past them are not computed or not seen
+ *                kv_lens: new tokens past max_q are not computed, keys from
+ *                max_kv on not seen
  *   window       0 for none; needs causal
  *   workspace    qgemm_kv8_attention_workspace(...) bytes, 16-byte aligned
  *                (may be NULL if that is 0); contents undefined before and
