@@ -445,7 +445,9 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
  *   block_table, cu_seqlens, kv_lens   as for the append
  *   max_q, max_kv   at least the largest count of new tokens and the largest
  *                kv_lens: new tokens past max_q are not computed, keys from
- *                max_kv on not seen
+ *                max_kv on not seen.  max_q below 2^24, and no more than 65535
+ *                splits times tiles of 128 rows (new tokens x heads / kv_heads;
+ *                256 where head_dim is 128), else QGEMM_ERR_BAD_SHAPE
  *   window       0 for none; needs causal
  *   workspace    qgemm_kv8_attention_workspace(...) bytes, 16-byte aligned
  *                (may be NULL if that is 0); contents undefined before and

@@ -185,3 +185,9 @@ def test_matvec_refusals_by_kind_empty_and_device(monkeypatch):
     monkeypatch.setenv("QGEMM_FAKE_ARCH", "gfx950")
     monkeypatch.setenv("QGEMM_INJECT_LAUNCH_ERROR", "719")
     assert i4() == q.QGEMM_ERR_HIP and mx() == q.QGEMM_ERR_HIP
+
+
+def test_attention_limits_are_named():
+    for kw in (dict(max_q=1 << 24, tokens=1 << 24), dict(max_q=1 << 23, tokens=1 << 23, heads=16, ldq=1024, ldo=1024)):
+        assert attend(**kw, ws=A, nbytes=1 << 60) == q.QGEMM_ERR_BAD_SHAPE
+        assert b"max_q" in q.lib().qgemm_last_error()
