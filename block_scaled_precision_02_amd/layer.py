@@ -31,6 +31,23 @@ def _enqueue(entry, device, stream, *args):
         _check(status)
 
 
+def _new(shape, dtype, device, stream, returned=True):
+    """An uninitialised tensor that work on stream will write.  Memory of another
+    stream's pool may still be in use by that stream's earlier work, so it
+    comes from the given stream's own; what the caller gets is kept, once let go,
+    until the current stream has used it too."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    own = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(own):
+        t = _empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _rows(t, name, dtypes=_BF16):
     """Shape and row stride (elements) of a 2-D GPU tensor with unit stride
     along its rows."""
@@ -53,7 +70,7 @@ def _vec(t, name, n, device, dtypes=_BF16):
 
 # ------------------------------------------------------------ RMS norm
 
-def _norm_common(X, gamma, residual, residual_out):
+def _norm_common(X, gamma, residual, residual_out, stream):
     """What the four norms share: (shape, device, the arguments up to gamma,
     residual_out, its pointer and stride)."""
     shape, ldx = _rows(X, "X")
@@ -65,7 +82,7 @@ def _norm_common(X, gamma, residual, residual_out):
             raise ValueError(f"residual must be {tuple(shape)} on {device}, got {tuple(rshape)} on {residual.device}")
         pr = residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty(shape, dtype=torch.bfloat16, device=device)
+            residual_out = _new(shape, torch.bfloat16, device, stream)
     if residual_out is not None:
         oshape, ldo = _rows(residual_out, "residual_out")
         if oshape != shape or residual_out.device != device:
@@ -76,11 +93,11 @@ def _norm_common(X, gamma, residual, residual_out):
             residual_out, po or None, ldo)
 
 
-def _norm_codes(out, M, row, device, dtype):
+def _norm_codes(out, M, row, device, dtype, stream):
     """The codes' tensor and row stride in bytes."""
     if out is None:
         wide = row + (-row) % 16          # the library's rule for row strides
-        out = _empty((M, wide), dtype=dtype, device=device)
+        out = _new((M, wide), dtype, device, stream)
         return (out if wide == row else out[:, :row]), wide
     if dtype is torch.int8:
         if tuple(out.shape) != (M, row) or out.dtype != torch.int8 or out.device != device or (
@@ -92,10 +109,10 @@ def _norm_codes(out, M, row, device, dtype):
 
 
 def _norm_row(entry, dtype, X, gamma, eps, residual, residual_out, out, scale, stream):
-    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out)
-    out, ldq = _norm_codes(out, M, K, device, dtype)
+    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out, stream)
+    out, ldq = _norm_codes(out, M, K, device, dtype, stream)
     if scale is None:
-        scale = _empty(M, dtype=torch.float32, device=device)
+        scale = _new(M, torch.float32, device, stream)
         ps = scale.data_ptr()
     else:
         ps = _vec(scale, "scale", M, device, (torch.float32,))
@@ -122,10 +139,10 @@ def qgemm_rmsnorm_quant_f8_pertoken(X, gamma, eps=1e-6, residual=None, residual_
 
 
 def _norm_block(entry, first, row, parts, dtype, X, gamma, eps, residual, residual_out, out, scale, stream):
-    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out)
-    out, ldq = _norm_codes(out, M, row, device, torch.uint8)
+    (M, K), device, head, residual_out, po, ldo = _norm_common(X, gamma, residual, residual_out, stream)
+    out, ldq = _norm_codes(out, M, row, device, torch.uint8, stream)
     if scale is None:
-        scale, lds = _empty((M, parts), dtype=dtype, device=device), parts
+        scale, lds = _new((M, parts), dtype, device, stream), parts
     else:
         sshape, lds = _rows(scale, "scale", (dtype,))
         if tuple(sshape) != (M, parts) or scale.device != device:
@@ -275,7 +292,7 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
     tokens, heads, dim = shape
     pt, ldt, width, pc, pl, batch = _sequences(block_table, cu_seqlens, kv_lens, device)
     if out is None:
-        out, ldo = _empty(shape, dtype=torch.bfloat16, device=device), heads * dim
+        out, ldo = _new(shape, torch.bfloat16, device, stream), heads * dim
     else:
         oshape, ldo = _token_rows(out, "out", heads, dim, device, (torch.bfloat16,))
         if oshape != shape:
@@ -288,11 +305,9 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
     if workspace is None:
         nbytes = L.qgemm_kv8_attention_workspace(cache._ref, tokens, batch, heads, max_q, max_kv, causal, window)
         if nbytes > 0:
-            workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+            # let go here, it goes back to the stream that uses it
+            workspace = _new(nbytes, torch.uint8, device, stream, returned=False)
             pw = workspace.data_ptr()
-            if stream is not None:   # it is let go here, when the stream may not have come to it
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                        torch.cuda.ExternalStream(int(stream), device=device))
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     else:
@@ -304,7 +319,7 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
 
 # ------------------------------------------------------------ 4-bit matvec
 
-def _w4_args(X, W, bias, out):
+def _w4_args(X, W, bias, out, stream):
     (M, K), ldx = _rows(X, "X")
     (N, row), ldw = _rows(W, "W", (torch.uint8,))
     if row * 2 != K:
@@ -314,7 +329,7 @@ def _w4_args(X, W, bias, out):
         raise ValueError(f"W must be on {device}, found on {W.device}")
     pb = None if bias is None else _vec(bias, "bias", N, device)
     if out is None:
-        out, ldy = _empty((M, N), dtype=torch.bfloat16, device=device), N
+        out, ldy = _new((M, N), torch.bfloat16, device, stream), N
     else:
         oshape, ldy = _rows(out, "out", (torch.bfloat16,))
         if tuple(oshape) != (M, N) or out.device != device:
@@ -332,7 +347,7 @@ def qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None, stream=Non
     """bf16 X [M, K] (M <= 64) times int4 weights W uint8 [N, K/2] with bf16
     scales and uint8 zero points (8 where None) per group: both
     [N, K/group], group 32, 64 or 128 -> bf16 [M, N]."""
-    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out)
+    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out, stream)
     groups = scales.shape[1] if scales.dim() == 2 else 0
     if groups == 0 or K % groups:
         raise ValueError(f"scales must be [{N}, K/group], got {tuple(scales.shape)} for K={K}")
@@ -350,7 +365,7 @@ def qgemm_w4_matvec_mx(X, W, scale_b, b_layout, bias=None, out=None, stream=None
     """bf16 X [M, K] (M <= 64) times the MXFP4 B operand of qgemm_mx: W uint8
     [N, K/2] e2m1, scale_b ue8m0 [N, K/32] (b_layout 1) or [ceil(N/32), K/32]
     (b_layout 32) -> bf16 [M, N]."""
-    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out)
+    device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out, stream)
     rows = -(-N // b_layout) if b_layout in (1, 32) else N
     ps = _w4_table(scale_b, "scale_b", (rows, K // 32), _UE8M0, device)
     _enqueue(lib().qgemm_w4_matvec_mx, device, stream, px, ldx, pw, ldw, ps, b_layout, pb, out.data_ptr(), ldy, M, N,
