@@ -468,7 +468,8 @@ def _codes_out(out, shape, device, name):
     if out is None:
         # rows padded to a multiple of 16 bytes (the library's ldq rule)
         return torch.empty((M, row + (-row) % 16), dtype=torch.uint8, device=device)[:, :row]
-    if tuple(out.shape) != shape or out.dtype not in (torch.uint8, torch.float8_e4m3fn) or out.device != device:
+    if not isinstance(out, torch.Tensor) or tuple(out.shape) != shape or \
+            out.dtype not in (torch.uint8, torch.float8_e4m3fn) or out.device != device:
         raise ValueError(f"{name} must be uint8 {shape} on {device}")
     if row > 1 and out.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along K")

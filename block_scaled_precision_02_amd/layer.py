@@ -100,7 +100,7 @@ def _norm_codes(out, M, row, device, dtype, stream):
         out = _new((M, wide), dtype, device, stream)
         return (out if wide == row else out[:, :row]), wide
     if dtype is torch.int8:
-        if tuple(out.shape) != (M, row) or out.dtype != torch.int8 or out.device != device or (
+        if not isinstance(out, torch.Tensor) or tuple(out.shape) != (M, row) or out.dtype != torch.int8 or out.device != device or (
                 row > 1 and out.stride(1) != 1):
             raise ValueError(f"out must be int8 [{M}, {row}] with unit stride along K on {device}")
     else:
@@ -156,7 +156,7 @@ def qgemm_rmsnorm_quant_f8_block(X, gamma, eps=1e-6, residual=None, residual_out
     """RMS norm of X + residual -> (e4m3 codes as uint8 [M, K], scales fp32
     [M, K/128], the sum in bf16): the A operand and scale_a of
     qgemm_f8_blockscale.  K a multiple of 128."""
-    K = X.shape[-1]
+    K = _rows(X, "X")[0][1]
     if K % 128:
         raise ValueError(f"K={K} is not a multiple of 128")
     return _norm_block(lib().qgemm_rmsnorm_quant_f8_block, (), K, K // 128, torch.float32, X, gamma, eps, residual,
@@ -170,7 +170,7 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
     scale_a of qgemm_mx."""
     if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
         raise ValueError(f"unknown MX format {fmt}")
-    K = X.shape[-1]
+    K = _rows(X, "X")[0][1]
     return _norm_block(lib().qgemm_rmsnorm_quant_mx, (fmt,), K if fmt == QGEMM_MX_E4M3 else K // 2, K // 32,
                        torch.uint8, X, gamma, eps, residual, residual_out, out, scale, stream)
 
@@ -229,6 +229,13 @@ class KV8Cache:
                    torch.empty((num_blocks, kv_heads), dtype=torch.float32, device=device))
 
 
+def _cache(cache):
+    """The cache's device."""
+    if not isinstance(cache, KV8Cache):
+        raise ValueError(f"cache must be a KV8Cache, got {type(cache).__name__}")
+    return cache.device
+
+
 def _token_rows(t, name, heads, dim, device, dtypes=_BF16):
     """Shape and token stride (elements) of a [tokens, heads, dim] tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
@@ -244,6 +251,8 @@ def _token_rows(t, name, heads, dim, device, dtypes=_BF16):
 def _sequences(table, cu, lens, device):
     """(table pointer, stride, width), cu pointer, lens pointer, batch."""
     i32 = torch.int32
+    if not (isinstance(table, torch.Tensor) and isinstance(cu, torch.Tensor) and isinstance(lens, torch.Tensor)):
+        raise ValueError("block_table, cu_seqlens and kv_lens must be tensors")
     if table.dtype != i32 or cu.dtype != i32 or lens.dtype != i32 or table.device != device or cu.device != device \
             or lens.device != device:
         raise ValueError(f"block_table, cu_seqlens and kv_lens must be int32 on {device}")
@@ -268,7 +277,7 @@ def qgemm_kv8_append(cache, K, V, block_table, cu_seqlens, kv_lens, max_q, strea
     int32 [batch + 1] the offsets of each sequence's new tokens; kv_lens int32
     [batch] the lengths with them; max_q at least the most new tokens of a
     sequence."""
-    device = cache.device
+    device = _cache(cache)
     kshape, ldk = _token_rows(K, "K", cache.kv_heads, cache.head_dim, device)
     vshape, ldv = _token_rows(V, "V", cache.kv_heads, cache.head_dim, device)
     if vshape != kshape:
@@ -287,7 +296,7 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
     the last that many positions of each token.  workspace: a uint8 tensor of
     at least qgemm_kv8_attention_workspace(...) bytes, allocated here if not
     given.  Tokens of no sequence are left as they are in ``out``."""
-    device = cache.device
+    device = _cache(cache)
     shape, ldq = _token_rows(Q, "Q", None, cache.head_dim, device)
     tokens, heads, dim = shape
     pt, ldt, width, pc, pl, batch = _sequences(block_table, cu_seqlens, kv_lens, device)
@@ -308,7 +317,7 @@ def qgemm_kv8_attention(cache, Q, block_table, cu_seqlens, kv_lens, max_q, max_k
             # let go here, it goes back to the stream that uses it
             workspace = _new(nbytes, torch.uint8, device, stream, returned=False)
             pw = workspace.data_ptr()
-    elif workspace.device != device or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     else:
         pw, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -338,7 +347,7 @@ def _w4_args(X, W, bias, out, stream):
 
 
 def _w4_table(t, name, shape, dtypes, device):
-    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be {dtypes} {shape}, contiguous, on {device}")
     return t.data_ptr()
 
@@ -348,9 +357,9 @@ def qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None, stream=Non
     scales and uint8 zero points (8 where None) per group: both
     [N, K/group], group 32, 64 or 128 -> bf16 [M, N]."""
     device, px, ldx, pw, ldw, M, N, K, pb, out, ldy = _w4_args(X, W, bias, out, stream)
-    groups = scales.shape[1] if scales.dim() == 2 else 0
+    groups = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 2 else 0
     if groups == 0 or K % groups:
-        raise ValueError(f"scales must be [{N}, K/group], got {tuple(scales.shape)} for K={K}")
+        raise ValueError(f"scales must be a tensor [{N}, K/group] for K={K}, got {getattr(scales, 'shape', scales)}")
     ps = _w4_table(scales, "scales", (N, groups), _BF16, device)
     pz = None if zeros is None else _w4_table(zeros, "zeros", (N, groups), (torch.uint8,), device)
     _enqueue(lib().qgemm_w4_matvec_i4, device, stream, px, ldx, pw, ldw, ps, pz, K // groups, pb, out.data_ptr(), ldy,
