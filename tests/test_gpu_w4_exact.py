@@ -154,3 +154,45 @@ def test_tables_that_are_not_16_byte_aligned(kind, group, M):
             d[n] = buf[1:].view(d[n].shape)
             assert d[n].data_ptr() % 16
     check(kind, d, group)
+
+
+# A workgroup that walks over several tiles of weights (256 or 512 workgroups of
+# 16 rows each), whose last tile is not whole; K of 8, 57 and 64 chunks, the
+# longest in parts above four rows.
+@pytest.mark.parametrize("M", [1, 3, 4, 8, 16])
+@pytest.mark.parametrize("N,K", [(8203, 1024), (12337, 7296), (20011, 8192)])
+@pytest.mark.parametrize("kind,group,zeros,srows", [("i4", 32, True, 1), ("i4", 32, False, 1), ("i4", 64, True, 1),
+                                                    ("i4", 64, False, 1), ("i4", 128, True, 1), ("i4", 128, False, 1),
+                                                    ("mx", 32, False, 1), ("mx", 32, False, 32)])
+def test_several_tiles_a_workgroup(kind, group, zeros, srows, M, N, K):
+    check(kind, make(kind, M, N, K, group, M + N, zeros, True, srows), group, srows)
+
+
+# Above 16 rows: one and two tiles of weights a wave, last tiles that are not
+# whole, K that ends inside a chunk and K > 8192.
+@pytest.mark.parametrize("M", [17, 32, 33, 64])
+@pytest.mark.parametrize("N,K", [(8192, 1056), (8209, 8320), (530, 10240)])
+@pytest.mark.parametrize("kind,group,zeros,srows", [("i4", 32, True, 1), ("i4", 64, False, 1), ("i4", 128, True, 1),
+                                                    ("mx", 32, False, 1), ("mx", 32, False, 32)])
+def test_many_rows(kind, group, zeros, srows, M, N, K):
+    K = K // group * group
+    check(kind, make(kind, M, N, K, group, M + N, zeros, True, srows), group, srows)
+
+
+@pytest.mark.parametrize("M", [1, 4, 5, 16])
+@pytest.mark.parametrize("K", [8320, 21504, 33024])
+@pytest.mark.parametrize("kind,group,zeros", [("i4", 32, False), ("i4", 64, True), ("i4", 128, True), ("mx", 32, False)])
+def test_long_rows(kind, group, zeros, M, K):
+    check(kind, make(kind, M, 517, K, group, M + K, zeros, True), group)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 12337, 5376), (16, 20011, 8192), (33, 8209, 2048), (1, 517, 21504)])
+@pytest.mark.parametrize("kind", ["i4", "mx"])
+def test_the_same_call_gives_the_same_bits(kind, M, N, K):
+    d = make(kind, M, N, K, 32, 1, kind == "i4")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    d["x"] = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    first = run(kind, d)
+    for _ in range(5):
+        assert torch.equal(run(kind, d), first)
