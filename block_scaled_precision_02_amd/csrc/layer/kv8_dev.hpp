@@ -87,18 +87,20 @@ __device__ __forceinline__ unsigned enc4(float a, float b, float c, float d)
 
 // What a block's V scale does to a probability, see kv8_stream.hip: its log2
 // and its reciprocal.  Where the scale is zero the codes are cleared
-// and the last other scale stands in (held: per lane, starts at 1).  A NaN
-// scale (an infinite one too) makes the logarithm NaN, and so the weights of the
-// rows that see its block, and theirs alone.
+// and the last other scale stands in (held: per lane, starts at 1).
 struct VScale {
     float log2, inv;
 };
 __device__ __forceinline__ VScale v_scale(float s, float &held)
 {
     if (s > 0.0f)
-        held = __builtin_amdgcn_fmed3f(s, 0x1p-100f, 0x1p127f);
-    return VScale{__builtin_amdgcn_logf(held) + (s - s), __builtin_amdgcn_rcpf(held)};
+        held = fmaxf(s, 0x1p-100f);
+    return VScale{__builtin_amdgcn_logf(held), __builtin_amdgcn_rcpf(held)};
 }
+
+// What a block's scores are multiplied by.  A NaN V scale makes it NaN, and so
+// the weights of the rows that see the block, and theirs alone.
+__device__ __forceinline__ float score_scale(float sk, float sv, float scale2) { return fmaf(sk, scale2, sv - sv); }
 
 // The weights enter the second product as binary16 between 0 and 2^15.
 constexpr float W_TOP = 15.0f;

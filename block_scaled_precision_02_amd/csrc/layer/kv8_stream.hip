@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(WAVES * 64, stream_occupancy(DC, NT)) kv8_stre
         if (more)
             load_k(s + WAVES, next_k);
         // (a scale of a block that is not there may be anything)
-        const float k_scale = vid >= 0 ? sk * a.scale2 : 0.0f, v_raw = vid >= 0 ? raw : 0.0f;
+        const float k_scale = vid >= 0 ? score_scale(sk, raw, a.scale2) : 0.0f, v_raw = vid >= 0 ? raw : 0.0f;
         const VScale sv = v_scale(v_raw, held);
 
         // a step that every row sees whole needs no mask; elsewhere the codes

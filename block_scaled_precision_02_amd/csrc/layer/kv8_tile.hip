@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(WAVES * 64, tile_occupancy(DC, WAVES)) kv8_til
             lk[buf][k_chunk<CH>(tok, c + 1)] = u32x4{w2[0], w2[1], w3[0], w3[1]};
         }
         // (a scale of a block that is not there may be anything)
-        r_sk = vid_now >= 0 ? r_sk * a.scale2 : 0.0f;
+        r_sk = vid_now >= 0 ? score_scale(r_sk, r_sv, a.scale2) : 0.0f;
         r_sv = vid_now >= 0 ? r_sv : 0.0f;
         // V codes that no row sees (0 * NaN), or whose scale is zero, are cleared
         const int vtok = s * STEP + (threadIdx.x & 3) * 16;   // the same for every piece of the thread
