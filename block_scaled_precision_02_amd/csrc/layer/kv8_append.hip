@@ -11,9 +11,10 @@
 // all bytes that its scale governs, so that no scale is seen half updated and
 // no atomics are needed.  A NaN or an infinity among the new values makes the
 // scale NaN, which the maximum hands on to later appends.  On one MI355X: 64 single tokens of 8 heads of 128
-// 5.2 us; six prompts, 19002 tokens in all, 36 to 38 us, 3.1 TB/s of the bytes they
-// need: a workgroup's loads, maximum, quotients and stores follow one another,
-// and five workgroups a CU cover for each other only in part (workgroups of 512
+// 6.2 to 6.7 us (5.2 the shortest); six prompts, 19002 tokens in all, 36 to 39 us,
+// 3.1 TB/s of the bytes they need: a workgroup's loads, maximum, quotients and
+// stores follow one another (waves wait for two thirds of their time, the vector
+// units issue for 16 us), and five workgroups a CU cover for each other only in part (workgroups of 512
 // threads 41 us, registers held to 6 waves a SIMD 58).  Bytes of tokens at or past the sequence's length
 // keep what they held.
 #include <hip/hip_runtime.h>

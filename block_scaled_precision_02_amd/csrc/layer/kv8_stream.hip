@@ -33,7 +33,8 @@
 //    are one pair a step.
 // On one MI355X: 64 sequences of up to 8192 tokens, 64 heads over 8 of 128, e4m3,
 // 152 us, 5.3 TB/s (reading alone: 6.5); three of 65537, 64 heads over 4, int8,
-// 44 us and 4.7 for the joining; one of 1001 11 us, which is latency (a chain of
+// 44 us (vector units issuing for 14 of them, waves waiting for three quarters of
+// their time, 1.4 of them a SIMD) and 4.8 for the joining; one of 1001 11 us, which is latency (a chain of
 // lengths, block number, codes, and two turns of a wave).
 // Q and the codes of K enter the first product as bf16, the codes of V the
 // second as binary16, all exactly; the sums are binary32.
@@ -66,7 +67,8 @@ __device__ __forceinline__ float groups_sum(float v)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Waves a SIMD that the registers are held to.
+// Waves a SIMD that the registers are held to, and that the plan counts on (the
+// 168 registers of D = 128 with one tile would let in a third one).
 constexpr int stream_occupancy(int dc, int nt)
 {
     return nt == 1 ? (dc == 1 ? 4 : dc <= 3 ? 2 : 1) : dc <= 2 ? 2 : 1;

@@ -17,12 +17,17 @@
 //    range): weights are 2^(x - reference + 7) with the reference up to 2^8 out
 //    of date, and most steps neither fade the sums nor touch the accumulators.
 // On one MI355X: a chunk of 4096 tokens over 8192, 32 heads over 8 of 128, e4m3,
-// 469 us, 880 TFLOP/s (a bf16 library product of 8192^3: 1323; 512 us with the
-// block numbers loaded together with the codes, which waited for them); five
-// prompts of up to 1777 tokens, 16 heads of 64, int8, window 1024, 71 us, 330
-// TFLOP/s, where the exponentials weigh twice as much; 192 and 256 channels, whose
-// accumulators leave one wave a SIMD and nothing to run beside its softmax, 375
-// and 354.
+// 454 to 480 us, 860 to 910 TFLOP/s (a bf16 library product of 8192^3: 1323; 512 us
+// with the block numbers loaded together with the codes, which waited for them).
+// Counters there: matrix cores busy 36% of the cycles, vector instructions (262 a
+// wave and step besides the 32 products; the softmax is about 225 of them) 41%, two
+// waves a SIMD, LDS 28%.  So the two overlap little: the barrier a step keeps both
+// waves of a SIMD in the same phase, and they wait for 44% of their time.  Five
+// prompts of up to 1777 tokens, 16 heads of 64, int8, window 1024, 69 us, 340
+// TFLOP/s: matrix cores 13%, vector instructions 40% (365 a wave and step, for
+// half the products), 1.8 of three waves a SIMD there, waiting 45% of their
+// time (928 workgroups on 768 places, a barrier a step).  192 and 256 channels,
+// whose accumulators leave one wave a SIMD, 375 and 354 TFLOP/s.
 // The rows of a kv head (its tokens times the heads that share it) are cut into
 // tiles of 32 a wave; a split of the keys, where there are few tiles, leaves
 // sums for kv8_join_kernel.
@@ -359,8 +364,10 @@ hipError_t launch_waves(const Kv8Attn &a, hipStream_t s)
 int kv8_tile_occupancy(int dc, int waves)
 {
     // eight waves, a step's codes shared by 256 rows: D = 128 (4096 tokens over
-    // 8192: 512 us against 541 with four, when that was measured; D = 64: 104 against 75, 5 prompts of
-    // up to 1777 tokens, where three workgroups of four are resident)
+    // 8192 480 us against 494 with four; four of up to 1000 over 1500 95 against
+    // 90; 512 over 2048 and 6 of up to 300 alike).  D = 64 four (five prompts of up
+    // to 1777 tokens 72 against 102 with eight, four of up to 1000 55 against 70,
+    // 4096 over 8192 alike), of which three workgroups are resident
     return waves == 4 || (waves == 8 && dc == 2) ? tile_occupancy(dc, waves) : 0;
 }
 

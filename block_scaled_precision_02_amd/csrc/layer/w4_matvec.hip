@@ -26,8 +26,10 @@
 // The workgroup's 8 waves split K and meet in LDS; the order of the sums is
 // fixed.
 // On one MI355X, weights not in a cache: 1x21504x5376 int4 in groups of 128 with
-// zero points 20.4 us, 3.0 TB/s; 1x8192x8192 MXFP4 10.7 us, 3.3 TB/s; 16x8192x8192
-// MXFP4 20 us, half of it x, which every workgroup lays out for itself.
+// zero points 20.4 us, 3.0 TB/s, 10 of them vector instructions, of which the
+// nibbles are three in five; 1x8192x8192 MXFP4 11.4 us, 3.1 TB/s; 16x8192x8192
+// MXFP4 20.5 us, in which the vector units issue for 4.4 and a wave waits for
+// three quarters of its time: every workgroup lays out all of x for itself.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -545,7 +547,8 @@ hipError_t launch_zeros(const W4Args &a, hipStream_t s)
     constexpr int NUM_CU = 256;
     const int tiles = (a.N + 15) / 16, chunks = (a.K + CHUNK - 1) / CHUNK;
     // as many workgroups as are resident: two a CU while LDS has room for both
-    // (4x8192x8192, 64 KB of x: one 14 us, two 18; 1x21504x5376: 20 and 18)
+    // (int4 in groups of 64, one and two: 4x8192x8192, 64 KB of x, 15.4 us and
+    // 19.7; 1x20000x2048 10.9 and 9.1; 1x21504x5376 23.0 and 21.8)
     int wgs = Lds::X <= 32768 && XR <= 4 ? 2 * NUM_CU : NUM_CU, kept = 0;
     if (chunks > W4_WAVES * CPW) {   // K in parts: no more tiles a workgroup than have room for their sums
         wgs = std::max(wgs, (tiles + Lds::KEPT - 1) / Lds::KEPT);

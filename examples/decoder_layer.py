@@ -27,6 +27,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import block_scaled_precision_02_amd as q  # noqa: E402
 
 E4M3, E2M1 = q.QGEMM_MX_E4M3, q.QGEMM_MX_E2M1
+# The matvec's most; it is the faster one here up to that (2048 x 7168, 64 rows:
+# 31 us against 44 for the quantiser and the GEMM; 17 rows: 14 against 40).
 MATVEC_ROWS = 64
 
 

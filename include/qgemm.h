@@ -456,7 +456,11 @@ qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, i
  * count as not visible.  Nothing of a block is read past the rows' visible
  * range that could reach the result: bytes there may hold anything, NaN codes
  * included; visible codes are finite, visible scales finite and >= 0, or NaN: a
- * row that sees a token of a block whose K or V scale is NaN becomes NaN. */
+ * row that sees a token of a block whose K or V scale is NaN becomes NaN.
+ * One call takes one kernel for all its sequences, the one for many rows where
+ * max_q x heads / kv_heads > 32: single tokens next to a prompt belong in a call of
+ * their own (63 over 8192 tokens and a prompt of 2048 over 4096, 32 heads over 8 of
+ * 128, on one MI355X: 165 and 167 us apart, 2067 us together). */
 int64_t qgemm_kv8_attention_workspace(const qgemm_kv8_cache *cache, int64_t tokens, int64_t batch, int64_t heads,
                                       int64_t max_q, int64_t max_kv, int causal, int64_t window);
 qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q, int64_t ldq,
@@ -466,7 +470,12 @@ qgemm_status qgemm_kv8_attention(const qgemm_kv8_cache *cache, const uint16_t *Q
                                  void *workspace, int64_t workspace_bytes, void *stream);
 
 /* A few rows of bf16 activations times 4-bit weights, for the projections of
- * decode steps (at most 64 rows; more rows: the GEMMs above).
+ * decode steps (at most 64 rows; more rows: the GEMMs above).  Which is faster
+ * below 64, MXFP4 on one MI355X, against quantising X and qgemm_mx_mixed: this
+ * one up to 64 rows at N x K = 8192 x 8192 (43 us and 49) and 2048 x 7168 (31 and
+ * 44), up to 32 at 14336 x 2048 (14 and 20; 64 rows: 25 and 21), up to 16 at
+ * 21504 x 5376 (31 and 43; 17 rows: 37 and 36), up to 4 at 5376 x 21504 (38 and
+ * 40; 8 rows: 48 and 46).
  *   X       [M, K] bf16, 0 <= M <= 64, row stride ldx elements (multiple of 8),
  *           16-byte aligned
  *   W       [N, K/2] bytes, weight k (k even) in bits 3:0 of byte k/2, k+1 in
