@@ -36,6 +36,22 @@ and the operators a decoder layer runs between its GEMMs (``layer.py``):
                         window=0, out=None, workspace=None)  -> O
     qgemm_w4_matvec_i4(X, W, scales, zeros=None, bias=None, out=None)
     qgemm_w4_matvec_mx(X, W, scale_b, b_layout, bias=None, out=None)
+    qgemm_postnorm_quant_i8_rowwise / _f8_pertoken / _f8_block
+        (Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None, out=None, scale=None)
+        -> (Q, scale, residual_out)
+    qgemm_postnorm_quant_mx(fmt, Y, residual, gamma_post, gamma, ...)
+
+and those of a layer of experts (``experts.py``):
+
+    qgemm_moe_sort(ids, experts)                          -> (offsets, order, position)
+    qgemm_moe_gather(X, position, rows=None, out=None)
+    qgemm_moe_combine(Y, position, weights=None, residual=None, out=None)
+    qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None)  -> (dY, dweights)
+    qgemm_i8_rowwise_grouped / qgemm_f8_pertoken_grouped / qgemm_f8_blockscale_grouped
+        (A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None)
+    qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None)
+    qgemm_swiglu_quant_i8_rowwise / _f8_pertoken / _f8_block (X, count=None, out=None, scale=None)  -> (Q, scale)
+    qgemm_swiglu_quant_mx(fmt, X, ...)
 
 Operands are [rows, K] with unit stride along K (row stride may exceed the
 row; it is passed as lda).  ``out`` may be a view of a wider buffer (row
@@ -74,6 +90,11 @@ EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f
            "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_f8_block",
            "qgemm_rmsnorm_quant_mx", "qgemm_kv8_append", "qgemm_kv8_attention", "qgemm_kv8_attention_workspace",
            "qgemm_w4_matvec_i4", "qgemm_w4_matvec_mx",
+           "qgemm_postnorm_quant_i8_rowwise", "qgemm_postnorm_quant_f8_pertoken", "qgemm_postnorm_quant_f8_block",
+           "qgemm_postnorm_quant_mx", "qgemm_moe_sort", "qgemm_moe_sort_workspace", "qgemm_moe_gather",
+           "qgemm_moe_combine", "qgemm_moe_combine_grad", "qgemm_swiglu_quant_i8_rowwise",
+           "qgemm_swiglu_quant_f8_pertoken", "qgemm_swiglu_quant_f8_block", "qgemm_swiglu_quant_mx",
+           "qgemm_i8_rowwise_grouped", "qgemm_f8_pertoken_grouped", "qgemm_f8_blockscale_grouped", "qgemm_mx_grouped",
            "qgemm_last_error", "qgemm_status_string", "qgemm_select_tile",
            "qgemm_tile_rows", "qgemm_force_tile")
 
@@ -159,6 +180,26 @@ def declare(L):
     L.qgemm_w4_matvec_i4.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P]
     L.qgemm_w4_matvec_mx.restype = st
     L.qgemm_w4_matvec_mx.argtypes = [_P, _I64, _P, _I64, _P, ctypes.c_int, _P, _P, _I64, _I64, _I64, _I64, _P]
+    for kind, tail in (("i8_rowwise", []), ("f8_pertoken", []), ("f8_block", [_I64]), ("mx", [_I64])):
+        head = [ctypes.c_int] if kind == "mx" else []
+        f = getattr(L, "qgemm_postnorm_quant_" + kind)
+        f.restype, f.argtypes = st, head + [_P, _P, _I64, _P] + tail + [_I64, _I64, _P]
+        f = getattr(L, "qgemm_swiglu_quant_" + kind)
+        f.restype, f.argtypes = st, head + [_P, _I64, _P, _P, _I64, _P] + tail + [_I64, _I64, _P]
+    L.qgemm_moe_sort_workspace.restype = _I64
+    L.qgemm_moe_sort_workspace.argtypes = [_I64, _I64, _I64]
+    L.qgemm_moe_sort.restype = st
+    L.qgemm_moe_sort.argtypes = [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P]
+    L.qgemm_moe_gather.restype = st
+    L.qgemm_moe_gather.argtypes = [_P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _P]
+    L.qgemm_moe_combine.restype = st
+    L.qgemm_moe_combine.argtypes = [_P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P]
+    L.qgemm_moe_combine_grad.restype = st
+    L.qgemm_moe_combine_grad.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]
+    grouped = [_P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _P]
+    for kind in ("i8_rowwise", "f8_pertoken", "f8_blockscale", "mx"):
+        f = getattr(L, f"qgemm_{kind}_grouped")
+        f.restype, f.argtypes = st, ([ctypes.c_int] if kind == "mx" else []) + grouped
     L.qgemm_last_error.restype = ctypes.c_char_p
     L.qgemm_last_error.argtypes = []
     L.qgemm_status_string.restype = ctypes.c_char_p
@@ -723,16 +764,27 @@ def qgemm_mx_prepacked(fmt, A, Bp, scale_a, scale_b, b_layout, bias=None, out=No
     return out
 
 
-# The decoder-layer operators live in layer.py, which needs torch at import;
-# they are looked up on first use, so that the package itself does not.
+# The decoder-layer operators live in layer.py, those of a layer of experts in
+# experts.py, which need torch at import; they are looked up on first use, so
+# that the package itself does not.
 _LAYER = ("KV8Cache", "qgemm_kv8_append", "qgemm_kv8_attention", "qgemm_rmsnorm_quant_f8_block",
           "qgemm_rmsnorm_quant_f8_pertoken", "qgemm_rmsnorm_quant_i8_rowwise", "qgemm_rmsnorm_quant_mx",
-          "qgemm_w4_matvec_i4", "qgemm_w4_matvec_mx")
+          "qgemm_w4_matvec_i4", "qgemm_w4_matvec_mx", "qgemm_postnorm_quant_f8_block",
+          "qgemm_postnorm_quant_f8_pertoken", "qgemm_postnorm_quant_i8_rowwise", "qgemm_postnorm_quant_mx")
+_EXPERTS = ("qgemm_moe_sort", "qgemm_moe_gather", "qgemm_moe_combine", "qgemm_moe_combine_grad",
+            "qgemm_swiglu_quant_i8_rowwise", "qgemm_swiglu_quant_f8_pertoken", "qgemm_swiglu_quant_f8_block",
+            "qgemm_swiglu_quant_mx", "qgemm_i8_rowwise_grouped", "qgemm_f8_pertoken_grouped",
+            "qgemm_f8_blockscale_grouped", "qgemm_mx_grouped")
 
 
 def __getattr__(name):
-    if name not in _LAYER:
+    if name in _LAYER:
+        from . import layer as module
+        names = _LAYER
+    elif name in _EXPERTS:
+        from . import experts as module
+        names = _EXPERTS
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layer
-    globals().update({n: getattr(layer, n) for n in _LAYER})
+    globals().update({n: getattr(module, n) for n in names})
     return globals()[name]

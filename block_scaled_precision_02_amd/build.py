@@ -20,12 +20,16 @@ LIB = os.path.join(HERE, "libqgemm.so")
 SOURCES = ["qgemm_api.cpp", "qgemm_i8.hip", "qgemm_f8.hip", "qgemm_mx8.hip", "qgemm_mx4.hip", "qgemm_f8b.hip", "qgemm_mx84.hip", "qgemm_mx48.hip", "qgemm_mx4h.hip", "qgemm_mx6.hip",
            "qgemm_quant.hip", "qgemm_pack.hip",
            "layer/layer_api.cpp", "layer/norm.hip", "layer/kv8_append.hip",
-           "layer/kv8_stream.hip", "layer/kv8_tile.hip", "layer/w4_matvec.hip"]
+           "layer/kv8_stream.hip", "layer/kv8_tile.hip", "layer/w4_matvec.hip", "layer/postnorm.hip",
+           "experts/experts_api.cpp", "experts/grouped.cpp", "experts/sort.hip", "experts/exchange.hip", "experts/swiglu.hip",
+           "experts/grouped_i8.hip", "experts/grouped_f8.hip", "experts/grouped_f8b.hip", "experts/grouped_mx8.hip",
+           "experts/grouped_mx4.hip"]
 # Per-source extra flags.  The blockscale kernel folds its MFMA partial sums
 # into the totals with VALU FMAs every 128 K elements; keeping the MFMA
 # results in VGPRs (rather than the accumulator registers, which the VALU
 # reaches only through a v_accvgpr_read per value) halves that VALU work.
-EXTRA_FLAGS = {"qgemm_f8b.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_FLAGS = {"qgemm_f8b.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "experts/grouped_f8b.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-fno-fast-math", "-Wall", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -20,6 +20,20 @@ struct NormArgs {
 };
 hipError_t launch_rmsnorm_quant(int out, const NormArgs &a, hipStream_t s);
 
+// The norm after a block, gate and residual scale, and the norm before the
+// next block with output as above.
+struct PostnormArgs {
+    const uint16_t *Y, *R;           // bf16 [M, K]
+    const uint16_t *gpost, *gate, *gamma;   // bf16 [K]; gate NULL: ones
+    uint16_t *Rout;
+    uint8_t *Q;
+    void *S;
+    int64_t ldy, ldr, ldo, ldq, lds;
+    int M, K;
+    float eps, alpha;
+};
+hipError_t launch_postnorm_quant(int out, const PostnormArgs &a, hipStream_t s);
+
 // The paged 8-bit cache (kv8_dev.hpp has the layout).
 enum Kv8Fmt { KV8_E4M3 = 0, KV8_I8 = 1 };
 struct Kv8Append {

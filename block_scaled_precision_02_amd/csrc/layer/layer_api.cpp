@@ -23,10 +23,8 @@ qgemm_status check_rows(const char *name, const void *p, int64_t ld, int64_t K)
     return QGEMM_OK;
 }
 
-// out: NormOut; the scale array's alignment and row length are the caller's.
-qgemm_status norm_common(int out, const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
-                         const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo, void *Q, int64_t ldq, void *S,
-                         int64_t lds, int64_t s_row, int64_t M, int64_t K, void *stream)
+// The shape of a norm with quantised output.
+qgemm_status check_norm_shape(int out, float eps, int64_t M, int64_t K)
 {
     if (M < 0 || K <= 0)
         return fail(QGEMM_ERR_BAD_SHAPE, "M=%lld K=%lld: need M>=0, K>0", (long long)M, (long long)K);
@@ -37,14 +35,12 @@ qgemm_status norm_common(int out, const uint16_t *X, int64_t ldx, const uint16_t
         return fail(QGEMM_ERR_BAD_SHAPE, "M and K must stay below 2^31");
     if (!(eps >= 0.0f))
         return fail(QGEMM_ERR_BAD_SHAPE, "eps=%g: need a number >= 0", (double)eps);
-    if (M == 0)
-        return QGEMM_OK;
-    TRY(check_rows("X", X, ldx, K));
-    if (R)
-        TRY(check_rows("R", R, ldr, K));
-    if (Rout)
-        TRY(check_rows("Rout", Rout, ldo, K));
-    TRY(check_rows("gamma", gamma, K, K));
+    return QGEMM_OK;
+}
+
+// Its codes and scales.
+qgemm_status check_norm_out(int out, const void *Q, int64_t ldq, const void *S, int64_t lds, int64_t s_row, int64_t K)
+{
     if (!Q)
         return fail(QGEMM_ERR_NULL_POINTER, "Q is NULL");
     const int64_t q_row = out == NORM_MX_E2M1 ? K / 2 : K;
@@ -58,9 +54,52 @@ qgemm_status norm_common(int out, const uint16_t *X, int64_t ldx, const uint16_t
         return fail(QGEMM_ERR_BAD_LAYOUT, "the scale array is not 4-byte aligned");
     if (out >= NORM_F8_BLOCK && (lds < s_row || lds >= LD_LIMIT))
         return fail(QGEMM_ERR_BAD_LAYOUT, "lds=%lld: need >= %lld, below 2^31", (long long)lds, (long long)s_row);
+    return QGEMM_OK;
+}
+
+// out: NormOut; the scale array's alignment and row length are the caller's.
+qgemm_status norm_common(int out, const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                         const uint16_t *gamma, float eps, uint16_t *Rout, int64_t ldo, void *Q, int64_t ldq, void *S,
+                         int64_t lds, int64_t s_row, int64_t M, int64_t K, void *stream)
+{
+    TRY(check_norm_shape(out, eps, M, K));
+    if (M == 0)
+        return QGEMM_OK;
+    TRY(check_rows("X", X, ldx, K));
+    if (R)
+        TRY(check_rows("R", R, ldr, K));
+    if (Rout)
+        TRY(check_rows("Rout", Rout, ldo, K));
+    TRY(check_rows("gamma", gamma, K, K));
+    TRY(check_norm_out(out, Q, ldq, S, lds, s_row, K));
     TRY(check_device());
     const NormArgs a = {X, R, gamma, Rout, (uint8_t *)Q, S, ldx, ldr, ldo, ldq, lds, (int)M, (int)K, eps};
     return launch([&] { return launch_rmsnorm_quant(out, a, (hipStream_t)stream); });
+}
+
+qgemm_status postnorm_common(int out, const qgemm_postnorm *n, void *Q, int64_t ldq, void *S, int64_t lds,
+                             int64_t s_row, int64_t M, int64_t K, void *stream)
+{
+    if (!n)
+        return fail(QGEMM_ERR_NULL_POINTER, "the norm's arguments are NULL");
+    TRY(check_norm_shape(out, n->eps, M, K));
+    if (!std::isfinite(n->alpha))
+        return fail(QGEMM_ERR_BAD_SHAPE, "alpha is not finite");
+    if (M == 0)
+        return QGEMM_OK;
+    TRY(check_rows("Y", n->Y, n->ldy, K));
+    TRY(check_rows("R", n->R, n->ldr, K));
+    if (n->Rout)
+        TRY(check_rows("Rout", n->Rout, n->ldo, K));
+    TRY(check_rows("gamma_post", n->gamma_post, K, K));
+    if (n->gate)
+        TRY(check_rows("gate", n->gate, K, K));
+    TRY(check_rows("gamma", n->gamma, K, K));
+    TRY(check_norm_out(out, Q, ldq, S, lds, s_row, K));
+    TRY(check_device());
+    const PostnormArgs a = {n->Y, n->R, n->gamma_post, n->gate, n->gamma, n->Rout, (uint8_t *)Q, S, n->ldy, n->ldr,
+                            n->ldo, ldq, lds, (int)M, (int)K, n->eps, n->alpha};
+    return launch([&] { return launch_postnorm_quant(out, a, (hipStream_t)stream); });
 }
 
 // ------------------------------------------------------------ 8-bit cache
@@ -210,6 +249,33 @@ qgemm_status qgemm_rmsnorm_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t
         return fail(QGEMM_ERR_BAD_FORMAT, "unknown MX element format %d", (int)fmt);
     return norm_common(fmt == QGEMM_MX_E4M3 ? NORM_MX_E4M3 : NORM_MX_E2M1, X, ldx, R, ldr, gamma, eps, Rout, ldo, Q,
                        ldq, S, lds, K / 32, M, K, stream);
+}
+
+qgemm_status qgemm_postnorm_quant_i8_rowwise(const qgemm_postnorm *norm, int8_t *Q, int64_t ldq, float *scale,
+                                             int64_t M, int64_t K, void *stream)
+{
+    return postnorm_common(NORM_I8_ROW, norm, Q, ldq, scale, 0, 0, M, K, stream);
+}
+
+qgemm_status qgemm_postnorm_quant_f8_pertoken(const qgemm_postnorm *norm, uint8_t *Q, int64_t ldq, float *scale,
+                                              int64_t M, int64_t K, void *stream)
+{
+    return postnorm_common(NORM_F8_ROW, norm, Q, ldq, scale, 0, 0, M, K, stream);
+}
+
+qgemm_status qgemm_postnorm_quant_f8_block(const qgemm_postnorm *norm, uint8_t *Q, int64_t ldq, float *S, int64_t lds,
+                                           int64_t M, int64_t K, void *stream)
+{
+    return postnorm_common(NORM_F8_BLOCK, norm, Q, ldq, S, lds, K / 128, M, K, stream);
+}
+
+qgemm_status qgemm_postnorm_quant_mx(qgemm_mx_fmt fmt, const qgemm_postnorm *norm, void *Q, int64_t ldq, uint8_t *S,
+                                     int64_t lds, int64_t M, int64_t K, void *stream)
+{
+    if (fmt != QGEMM_MX_E4M3 && fmt != QGEMM_MX_E2M1)
+        return fail(QGEMM_ERR_BAD_FORMAT, "unknown MX element format %d", (int)fmt);
+    return postnorm_common(fmt == QGEMM_MX_E4M3 ? NORM_MX_E4M3 : NORM_MX_E2M1, norm, Q, ldq, S, lds, K / 32, M, K,
+                           stream);
 }
 
 qgemm_status qgemm_kv8_append(const qgemm_kv8_cache *cache, const uint16_t *K, int64_t ldk, const uint16_t *V,

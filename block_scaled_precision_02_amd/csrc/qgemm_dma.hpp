@@ -157,8 +157,11 @@ __device__ __forceinline__ typename PathTraits<PATH>::Frag dma_frag(const uint8_
 // that start off dword boundaries, and at K % 64 == 32 a last stage of 32 K
 // elements.  (One kernel template: the body moved into a device function
 // called from two kernels spilled.)
-template <int PATH, int WN, int TM, int TN, bool BIAS, int BROWS, int OUT, bool SU = false>
-__global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
+// GROUPED: one product per expert; the workgroup's tile lies in one expert's
+// rows, whose A rows are looked up through the order where there is one.
+template <int PATH, int WN, int TM, int TN, bool BIAS, int BROWS, int OUT, bool SU = false, bool GROUPED = false>
+__global__ void __launch_bounds__(128 * WN, 1)
+    qgemm_dma_kernel(const std::conditional_t<GROUPED, GroupedParams, Params> arg)
 {
     constexpr int WM = 2;
     constexpr int NW = WM * WN;                           // waves
@@ -300,10 +303,69 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
     const int wm = wave / WN, wn = wave % WN;
     const int h = lane >> 5, r32 = lane & 31;
 
-    int tm, tn;
-    tile_of(p, tm, tn);
+    // (grouped: the expert's own operands, C from the tile's first row on)
+    std::conditional_t<GROUPED, Params, int> own;
+    int tm = 0, tn;
+    int tile_rows = 0;
+    const int32_t *order = nullptr;                       // of the tile's rows
+    if constexpr (GROUPED) {
+        GroupedTile g;
+        if (!grouped_tile<BM>(arg, g))
+            return;
+        own = arg;
+        own.b_packed = 0;
+        own.B += (int64_t)g.expert * arg.b_expert;
+        own.C = (uint8_t *)own.C + (int64_t)g.row0 * own.ldc * 2;
+        if constexpr (BIAS)
+            own.bias += (int64_t)g.expert * own.N;
+        if constexpr (SCL)
+            own.mx_sb += (int64_t)g.expert * ((own.N + BROWS - 1) / BROWS) * own.kblocks;
+        else
+            own.scale_b += (int64_t)g.expert * own.N;
+        if (arg.order) {
+            order = arg.order + g.row0;
+        } else {
+            own.A += (int64_t)g.row0 * own.lda;
+            if constexpr (SCL)
+                own.mx_sa += (int64_t)g.row0 * own.kblocks;
+            else
+                own.scale_a += g.row0;
+        }
+        tn = g.tn;
+        tile_rows = g.rows;
+    }
+    const Params &p = [&]() -> const Params & {
+        if constexpr (GROUPED)
+            return own;
+        else
+            return arg;
+    }();
+    if constexpr (!GROUPED)
+        tile_of(p, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int rows_a = min(BM, p.M - m0), rows_b = min(BN, p.N - n0);
+    const int rows_a = GROUPED ? tile_rows : min(BM, p.M - m0), rows_b = min(BN, p.N - n0);
+    // Row of A that the tile's row r takes (r < rows_a; grouped: a row that A
+    // does not have is out of every range).
+    auto a_row = [&](int r) -> unsigned {
+        if constexpr (GROUPED) {
+            if (order)
+                return (unsigned)order[r] / (unsigned)arg.top_k;
+        }
+        return (unsigned)r;
+    };
+    // byte `add` of that row, rows ld bytes apart
+    auto a_at = [&](int r, int64_t ld, int add) -> unsigned {
+        if constexpr (GROUPED) {
+            if (order) {
+                const unsigned row = a_row(r);
+                return row < (unsigned)arg.a_rows ? (unsigned)(row * ld + add) : OOB;
+            }
+        }
+        return (unsigned)(r * ld + add);
+    };
+    int src_rows = rows_a;                                // rows that the A descriptors cover
+    if constexpr (GROUPED)
+        src_rows = order ? (int)arg.a_rows : rows_a;
 
     // K is a whole number of stages (SU: possibly ending in half a stage);
     // the last round may hold fewer than four.  Its stages at or past K are
@@ -315,7 +377,7 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
     const int nfetch = F6 ? (p.kbytes + DSTAGE - 1) / DSTAGE : nst;
     const uint8_t *const a_base = p.A + (int64_t)m0 * p.lda;
     const int kbytes_a = A4 ? p.kbytes / 2 : p.kbytes;   // (A4 / B4: p.kbytes is K, a byte per element)
-    const uint32_t a_range = (uint32_t)((rows_a - 1) * p.lda + kbytes_a);
+    const uint32_t a_range = (uint32_t)((src_rows - 1) * p.lda + kbytes_a);
     // B row-major, or prepacked: 16-row groups of 1 KB blocks (32-row groups
     // for the mixed path's 32-byte B rows), block t of a group holding its
     // rows' K piece t already in this kernel's LDS order, so that a fetch
@@ -340,11 +402,11 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
             // i/2, the chunk of slot i%2
             const int r4 = AROWS_PER_FETCH * (DMA_A * wave + j) + (lane >> 1);
             const int c4 = (lane & 1) ^ ((r4 >> 3) & 1);
-            a_off[j] = r4 < rows_a ? (unsigned)(r4 * p.lda + 16 * c4) : OOB;
+            a_off[j] = r4 < rows_a ? a_at(r4, p.lda, 16 * c4) : OOB;
         } else {
             const int r = 16 * (DMA_A * wave + j) + (lane >> 2);
             const int c = (lane & 3) ^ ((r >> 2) & 3);
-            a_off[j] = r < rows_a ? (unsigned)(r * p.lda + 16 * c) : OOB;
+            a_off[j] = r < rows_a ? a_at(r, p.lda, 16 * c) : OOB;
         }
     }
 #pragma unroll
@@ -386,11 +448,11 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
             if constexpr (A4) {
                 const int r = 16 * (DPA * wave + j) + (lane >> 2);
                 const int q = (lane & 3) ^ ((r >> 2) & 3);
-                pa_off[j] = r < rows_a ? (unsigned)(r * p.lda + 16 * q) : OOB;
+                pa_off[j] = r < rows_a ? a_at(r, p.lda, 16 * q) : OOB;
             } else {
                 const int r = 8 * (DPA * wave + j) + (lane >> 3);
                 const int q = (lane & 7) ^ ((r >> 1) & 7);
-                pa_off[j] = r < rows_a ? (unsigned)(r * p.lda + 16 * q) : OOB;
+                pa_off[j] = r < rows_a ? a_at(r, p.lda, 16 * q) : OOB;
             }
         }
 #pragma unroll
@@ -516,12 +578,12 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
         // last tile of A, or of B's scale rows), and the dword's other bytes
         // lie in the same page; they land past the row's K/32 scales, where
         // the round's masking replaces them.
-        rsa = make_rsrc(p.mx_sa + (int64_t)m0 * p.kblocks, (uint32_t)((rows_a * p.kblocks + 3) & ~3));
+        rsa = make_rsrc(p.mx_sa + (int64_t)m0 * p.kblocks, (uint32_t)((src_rows * p.kblocks + 3) & ~3));
         const int srows_b = (rows_b + BROWS - 1) / BROWS;
         rsb = make_rsrc(p.mx_sb + (int64_t)(n0 / BROWS) * p.kblocks, (uint32_t)((srows_b * p.kblocks + 3) & ~3));
         const int sw = NW == 8 ? (wave & 3) : wave;               // scale row group of this wave
         const int ra_row = 64 * sw + lane;                         // A scale row of this lane
-        sa_fo = ra_row < rows_a ? (unsigned)(ra_row * p.kblocks) & ~3u : OOB;
+        sa_fo = ra_row < rows_a ? a_at(ra_row, p.kblocks, 0) & ~3u : OOB;
         const int rb_row = BROWS == 1 ? 64 * sw + lane : lane;     // 32 / 128 rows: rows 0..63, fetched alike by every wave
         sb_fo = rb_row < srows_b ? (unsigned)(rb_row * p.kblocks) & ~3u : OOB;
     }
@@ -541,8 +603,12 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
                 const bool a = g < NWA;
                 const int row = WRPF * (a ? g : g - NWA) + lane / LPR;
                 sw_a[e * NSCW + k] = a;
-                sw_off[e * NSCW + k] =
-                    row < (a ? rows_a : rows_b) ? (unsigned)(row * p.kblocks + 16 * (lane % LPR)) : OOB;
+                if (GROUPED && a)
+                    sw_off[e * NSCW + k] =
+                        row < rows_a ? a_at(row, p.kblocks, 16 * (lane % LPR)) : OOB;
+                else
+                    sw_off[e * NSCW + k] =
+                        row < (a ? rows_a : rows_b) ? (unsigned)(row * p.kblocks + 16 * (lane % LPR)) : OOB;
                 sw_dst[e * NSCW + k] = a ? 1024 * g : SAW * RW + 1024 * (g - NWA);
             }
     }
@@ -889,12 +955,21 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
     // scale chunk 0, stages 0..2 and the A rows of stage 3 (FP6: lines 0..3);
     // wait for stage 0 (line 0).
     if constexpr (PRM) {
-        if (wave == 0 && !SCL)
+        if (wave == 0 && !SCL && !GROUPED)
             dma16(make_rsrc(p.scale_a + m0, (uint32_t)(rows_a * 4)), 16 * lane, &lds[PRM_OFF]);
         if (wave == 1 && !SCL)
             dma16(make_rsrc(p.scale_b + n0, (uint32_t)(rows_b * 4)), 16 * lane, &lds[PRM_OFF + PRM_SB]);
         if (wave == 2 && BIAS)
             dma16(make_rsrc(p.bias + n0, (uint32_t)(rows_b * 2)), 16 * lane, &lds[PRM_OFF + PRM_BIAS]);
+    }
+    // (grouped: the rows' scales one by one, through the order)
+    constexpr bool GSA = GROUPED && PRM && !SCL;
+    float row_scale = 0.0f;
+    if constexpr (GSA) {
+        if (tid < rows_a) {
+            const unsigned row = a_row(tid);
+            row_scale = !order || row < (unsigned)arg.a_rows ? p.scale_a[row] : 0.0f;
+        }
     }
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
@@ -920,6 +995,10 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
             fetch_part(3, I0());
     }
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (GSA) {
+        if (tid < BM)
+            *(float *)&lds[PRM_OFF + 4 * tid] = row_scale;
+    }
     twin_sync();
     wait_vmcnt<PAIR ? (P6 ? 2 * NPF : PH ? NPF / 2 : NPF) : (F6 ? 3 : 2) * NDMA + (SPLIT ? DMA_A : 0)>();
     lds_barrier();
@@ -1140,7 +1219,7 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
     // 0.3937.  INT8 30000x21504x5376 2.817 -> 2.837, e2m1 in 64-element stages
     // 8192x8192x8256 0.4261 -> 0.4267, MXFP8 and e4m3 x e2m1 level: those
     // paths do not prefetch.)
-    constexpr bool SUCC = PATH == PATH_MX4 || F6 || BS;
+    constexpr bool SUCC = (PATH == PATH_MX4 || F6 || BS) && !GROUPED;
     constexpr int NT = 64 * NW;
     constexpr int WPC = sizeof(lds) > 80 * 1024 ? 1 : 2;           // workgroups per CU (LDS)
     constexpr int NXT = 8 * 32 * WPC;
@@ -1217,7 +1296,7 @@ __global__ void __launch_bounds__(128 * WN, 1) qgemm_dma_kernel(const Params p)
         }
     }
 
-    store_tile<PATH, WM, WN, TM, TN, BIAS, OUT, ((B4 || A4 || F6) ? BODY : OPND_BYTES), PRM>(p, acc, &lds[0], &lds[PRM_OFF], m0, n0,
+    store_tile<PATH, WM, WN, TM, TN, BIAS, OUT, ((B4 || A4 || F6) ? BODY : OPND_BYTES), PRM, GROUPED>(p, acc, &lds[0], &lds[PRM_OFF], m0, n0,
                                                                             rows_a, rows_b);
     // (the prefetched values, consumed here so that the loads stay: the wait
     // for them falls after the output stores)

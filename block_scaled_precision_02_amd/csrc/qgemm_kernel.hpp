@@ -86,6 +86,17 @@ struct Params {
     int c_cached;                  // full tiles store C through the caches (else non-temporal)
 };
 
+// Grouped products (one per expert, over its rows of the sorted choices): A, C
+// and the scales of A as above with M the room for rows; B, its scales and the
+// bias those of expert 0, the others following.
+struct GroupedParams : Params {
+    const int32_t *offsets;        // [experts + 1]: expert e has rows offsets[e] .. offsets[e+1]-1
+    const int32_t *order;          // [M]: row r takes row order[r] / top_k of A; null: row r
+    int64_t b_expert;              // bytes from one expert's B to the next
+    int64_t a_rows;                // rows of A
+    int top_k, experts;
+};
+
 constexpr int KSTEP_BYTES = 128;
 constexpr int CHUNKS = KSTEP_BYTES / 16;   // 16-byte chunks per staged row
 constexpr unsigned OOB = 0x80000000u;      // offset beyond every range check
@@ -166,6 +177,63 @@ __device__ __forceinline__ void tile_of_index(int tiles_m, int tiles_n, int grou
 __device__ __forceinline__ void tile_of(const Params &p, int &tm, int &tn)
 {
     tile_of_index(p.tiles_m, p.tiles_n, p.group_m, (int)blockIdx.x, tm, tn);
+}
+
+// The row tiles of a grouped product are those of each expert in turn, ceil(its
+// rows / BM) of them.  Their number is known on the device alone: the grid has
+// room for the most there can be (tiles_m), and workgroups past the last tile
+// leave.  Every wave finds its tile by itself: lane l counts the tiles of an
+// even share of the experts, a scan over the lanes gives each share's first
+// one.  Offsets are clamped to the rows there is room for, so that no value in
+// them leads out of range.
+struct GroupedTile {
+    int expert, row0, rows, tn;    // rows row0 .. row0 + rows - 1 (at most BM), column tile tn
+};
+
+template <int BM>
+__device__ __forceinline__ bool grouped_tile(const GroupedParams &p, GroupedTile &g)
+{
+    const int lane = threadIdx.x & 63;
+    const int share = (p.experts + 63) >> 6;              // experts a lane
+    const int e0 = min(lane * share, p.experts), e1 = min(e0 + share, p.experts);
+    auto bound = [&](int e) { return min(max(p.offsets[e], 0), p.M); };
+    auto tiles = [&](int lo, int hi) { return hi > lo ? (hi - lo + BM - 1) / BM : 0; };
+    int n = 0;
+    int lo = bound(e0);
+    for (int e = e0; e < e1; ++e) {
+        const int hi = bound(e + 1);
+        n += tiles(lo, hi);
+        lo = hi;
+    }
+    int scan = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(scan, off);
+        scan += lane >= off ? v : 0;
+    }
+    const int total = __builtin_amdgcn_readlane(scan, 63);
+    if ((int)blockIdx.x >= total * p.tiles_n)
+        return false;
+    int tm;
+    tile_of_index(total, p.tiles_n, p.group_m, (int)blockIdx.x, tm, g.tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    g.tn = __builtin_amdgcn_readfirstlane(g.tn);
+    // the first lane whose share ends past tm, and the tile's place in it
+    const int owner = __builtin_ctzll(__ballot(scan > tm));
+    int left = tm - (__builtin_amdgcn_readlane(scan, owner) - __builtin_amdgcn_readlane(n, owner));
+    int e = owner * share;
+    lo = bound(e);
+    int hi = bound(e + 1);
+    while (left >= tiles(lo, hi) && e + 1 < p.experts) {
+        left -= tiles(lo, hi);
+        ++e;
+        lo = hi;
+        hi = bound(e + 1);
+    }
+    g.expert = e;
+    g.row0 = lo + left * BM;
+    g.rows = min(BM, hi - g.row0);
+    return g.rows > 0;
 }
 
 template <int PATH> struct PathTraits;
@@ -311,7 +379,10 @@ constexpr int pow2_at_least(int x) { return x <= 1 ? 1 : 2 * pow2_at_least((x + 
 // LDSBYTES is the LDS at lds_base the kernel owns (reused as the output
 // stash once every wave is done with the operand buffers); prm is the
 // parked epilogue operands (used by full tiles when PRM).
-template <int PATH, int WM, int WN, int TM, int TN, bool BIAS, int OUT, int LDSBYTES, bool PRM, class Acc>
+// GROUPED: a tile is full where its columns are (stores of rows past rows_a fall
+// out of the descriptor's range), and the parked row scales serve every tile.
+template <int PATH, int WM, int WN, int TM, int TN, bool BIAS, int OUT, int LDSBYTES, bool PRM, bool GROUPED = false,
+          class Acc>
 __device__ __forceinline__ void store_tile(const Params &p, Acc (&acc)[TM][TN], uint8_t *lds_base,
                                            const uint8_t *prm, int m0, int n0, int rows_a, int rows_b)
 {
@@ -333,7 +404,7 @@ __device__ __forceinline__ void store_tile(const Params &p, Acc (&acc)[TM][TN], 
     // is that the edge tile loads its operands and stores its results element
     // by element (columns past N inside a row of ldc must not be touched).
     constexpr int ESZ = (OUT == OUT_I32) ? 4 : 2;
-    const bool full = (rows_a == BM) && (rows_b == BN);
+    const bool full = (GROUPED || rows_a == BM) && (rows_b == BN);
     const int nloc_base = wn * TN * 32 + 4 * h;
     const __amdgpu_buffer_rsrc_t rc = make_rsrc((const uint8_t *)p.C + (int64_t)m0 * p.ldc * ESZ,
                                                 (uint32_t)((int64_t)rows_a * p.ldc * ESZ));
@@ -369,7 +440,7 @@ __device__ __forceinline__ void store_tile(const Params &p, Acc (&acc)[TM][TN], 
             sa[i] = 0.f;
             if constexpr (OUT == OUT_BF16 && !MX) {
                 const int mloc = arow + 32 * i;
-                if (PRM && FULL)
+                if (PRM && (FULL || GROUPED))
                     sa[i] = *(const float *)(prm + 4 * mloc);
                 else if (mloc < rows_a)
                     sa[i] = p.scale_a[m0 + mloc];

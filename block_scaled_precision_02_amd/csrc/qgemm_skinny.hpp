@@ -102,11 +102,12 @@ template <int PATH, int TM> constexpr int skinny_depth()
     return TM == 1 ? (PATH == PATH_I8 ? 16 : 8) : (PATH == PATH_I8 ? 8 : 4);
 }
 
-template <int PATH, int TM, int D, bool BIAS, int BROWS>
+// GROUPED: one product per expert, as in qgemm_dma.hpp.
+template <int PATH, int TM, int D, bool BIAS, int BROWS, bool GROUPED = false>
 __global__ void __launch_bounds__(64 * SK_WAVES,
                                   ((PATH == PATH_MX8 || PATH == PATH_MX4 || PATH == PATH_MX84 || PATH == PATH_F8B) &&
                                    TM == 1) ? 2 : 1)
-    qgemm_skinny_kernel(const Params p)
+    qgemm_skinny_kernel(const std::conditional_t<GROUPED, GroupedParams, Params> arg)
 {
     using T = SkinnyTraits<PATH>;
     using Frag = typename T::Frag;
@@ -120,12 +121,61 @@ __global__ void __launch_bounds__(64 * SK_WAVES,
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
 
-    int tm, tn;
-    tile_of(p, tm, tn);
+    // (grouped: the expert's own operands, C from the tile's first row on)
+    std::conditional_t<GROUPED, Params, int> own;
+    int tm = 0, tn;
+    int tile_rows = 0;
+    const int32_t *order = nullptr;                 // of the tile's rows
+    if constexpr (GROUPED) {
+        GroupedTile t;
+        if (!grouped_tile<BM>(arg, t))
+            return;
+        own = arg;
+        own.b_packed = 0;
+        own.B += (int64_t)t.expert * arg.b_expert;
+        own.C = (uint8_t *)own.C + (int64_t)t.row0 * own.ldc * 2;
+        if constexpr (BIAS)
+            own.bias += (int64_t)t.expert * own.N;
+        if constexpr (INK)
+            own.mx_sb += (int64_t)t.expert * ((own.N + BROWS - 1) / BROWS) * own.kblocks;
+        else
+            own.scale_b += (int64_t)t.expert * own.N;
+        if (arg.order) {
+            order = arg.order + t.row0;
+        } else {
+            own.A += (int64_t)t.row0 * own.lda;
+            if constexpr (INK)
+                own.mx_sa += (int64_t)t.row0 * own.kblocks;
+            else
+                own.scale_a += t.row0;
+        }
+        tn = t.tn;
+        tile_rows = t.rows;
+    }
+    const Params &p = [&]() -> const Params & {
+        if constexpr (GROUPED)
+            return own;
+        else
+            return arg;
+    }();
+    if constexpr (!GROUPED)
+        tile_of(p, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int rows_a = min(BM, p.M - m0), rows_b = min(BN, p.N - n0);
+    const int rows_a = GROUPED ? tile_rows : min(BM, p.M - m0), rows_b = min(BN, p.N - n0);
+    int src_rows = rows_a;                                // rows that the A descriptors cover
+    if constexpr (GROUPED)
+        src_rows = order ? (int)arg.a_rows : rows_a;
+    // Row of A that the tile's row r takes, r < rows_a; grouped: past src_rows
+    // where A does not have it.
+    auto a_src = [&](int r) -> unsigned {
+        if constexpr (GROUPED) {
+            if (order)
+                return (unsigned)order[r] / (unsigned)arg.top_k;
+        }
+        return (unsigned)r;
+    };
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A + (int64_t)m0 * p.lda,
-                                                (uint32_t)((rows_a - 1) * p.lda + p.kbytes));
+                                                (uint32_t)((src_rows - 1) * p.lda + p.kbytes));
     // B row-major, or prepacked (the workgroup's 16 columns are one packed
     // group: 64-byte K piece t of its rows is the 1 KB block t, row r's chunk
     // c at slot 4r + (c ^ ((r >> 2) & 3)); rows past N are zeros there)
@@ -133,11 +183,16 @@ __global__ void __launch_bounds__(64 * SK_WAVES,
     const __amdgpu_buffer_rsrc_t rb =
         p.b_packed ? make_rsrc(p.B + (int64_t)(n0 / 16) * 16 * p.kbytes, (uint32_t)(16 * p.kbytes))
                    : make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + kbytes_b));
-    unsigned a_row[TM];
+    unsigned a_row[TM], src[GROUPED ? TM : 1];
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = 16 * i + r16;
-        a_row[i] = r < rows_a ? (unsigned)(r * p.lda) : OOB;
+        if constexpr (GROUPED) {
+            src[i] = r < rows_a ? a_src(r) : ~0u;
+            a_row[i] = src[i] < (unsigned)src_rows ? (unsigned)(src[i] * p.lda) : OOB;
+        } else {
+            a_row[i] = r < rows_a ? (unsigned)(r * p.lda) : OOB;
+        }
     }
     const unsigned b_row = r16 < rows_b ? (unsigned)(r16 * p.ldb) : OOB;
     const unsigned b_slot = 16u * (4 * r16 + (g ^ ((r16 >> 2) & 3)));   // packed: this lane's slot
@@ -151,13 +206,16 @@ __global__ void __launch_bounds__(64 * SK_WAVES,
     __amdgpu_buffer_rsrc_t rsa, rsb;
     unsigned sa_row[TM], sb_row = OOB;
     if constexpr (INK) {
-        rsa = make_rsrc(p.mx_sa + (int64_t)m0 * p.kblocks, (uint32_t)(rows_a * p.kblocks));
+        rsa = make_rsrc(p.mx_sa + (int64_t)m0 * p.kblocks, (uint32_t)(src_rows * p.kblocks));
         const int sb0 = n0 / BROWS, sb_rows = (n0 + rows_b - 1) / BROWS - sb0 + 1;
         rsb = make_rsrc(p.mx_sb + (int64_t)sb0 * p.kblocks, (uint32_t)(sb_rows * p.kblocks));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = 16 * i + r16;
-            sa_row[i] = r < rows_a ? (unsigned)(r * p.kblocks) : OOB;
+            if constexpr (GROUPED)
+                sa_row[i] = src[i] < (unsigned)src_rows ? (unsigned)(src[i] * p.kblocks) : OOB;
+            else
+                sa_row[i] = r < rows_a ? (unsigned)(r * p.kblocks) : OOB;
         }
         if (r16 < rows_b)
             sb_row = (unsigned)(((n0 + r16) / BROWS - sb0) * p.kblocks);
@@ -298,7 +356,7 @@ __global__ void __launch_bounds__(64 * SK_WAVES,
     __amdgpu_buffer_rsrc_t rsbe, rsae, rbias;
     if constexpr (!INK) {
         rsbe = make_rsrc(p.scale_b + n0, (uint32_t)(rows_b * 4));
-        rsae = make_rsrc(p.scale_a + m0, (uint32_t)(rows_a * 4));
+        rsae = make_rsrc(p.scale_a + m0, (uint32_t)(src_rows * 4));
     }
     if constexpr (BIAS)
         rbias = make_rsrc(p.bias + n0, (uint32_t)(rows_b * 2));
@@ -321,7 +379,10 @@ __global__ void __launch_bounds__(64 * SK_WAVES,
         float sa = 1.0f;
         if constexpr (!INK)
             sa = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                               rsae, mloc < rows_a ? (unsigned)(mloc * 4) : OOB, 0, 0));
+                                               rsae,
+                                               GROUPED ? (src[GROUPED ? i : 0] < (unsigned)src_rows ? src[GROUPED ? i : 0] * 4 : OOB)
+                                               : mloc < rows_a ? (unsigned)(mloc * 4)
+                                                               : OOB, 0, 0));
         float f[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {

@@ -1,0 +1,297 @@
+"""A layer of experts: the choices in order of experts, tokens' rows to the
+experts and back with their gradients, the grouped GEMMs, and SwiGLU between
+them.  Argument marshalling for the C entry points of the same names; errors as
+in the package: ValueError for arguments, RuntimeError for the device."""
+import torch
+
+from . import QGEMM_MX_E2M1, QGEMM_MX_E4M3, lib
+from .layer import _BF16, _enqueue, _new, _norm_codes, _rows, _vec
+
+_I32 = torch.int32
+_F32 = (torch.float32,)
+
+
+def _out_rows(t, name, shape, device, stream):
+    """(tensor, row stride) of a bf16 output, allocated where not given."""
+    if t is None:
+        return _new(shape, torch.bfloat16, device, stream), shape[1]
+    oshape, ld = _rows(t, name, (torch.bfloat16,))
+    if tuple(oshape) != shape or t.device != device:
+        raise ValueError(f"{name} must be bfloat16 {shape} on {device}, got {tuple(oshape)} on {t.device}")
+    return t, ld
+
+
+def _choices(t, name):
+    """(tokens, top_k) of an int32 [tokens, top_k] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype != _I32 or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 GPU tensor [tokens, top_k]")
+    return t.shape
+
+
+# ------------------------------------------------------------ sort and exchange
+
+def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, workspace=None, stream=None):
+    """The choices ids int32 [tokens, top_k] in order of experts -> (offsets
+    int32 [experts + 1], order int32 [tokens * top_k], position int32
+    [tokens, top_k]): rows offsets[e] .. offsets[e+1]-1 are expert e's, row r is
+    slot order[r] (token order[r] // top_k), slot s is row position[s].  Ids
+    outside [0, experts) have no row (position -1; order -1 past the last row).
+    workspace: a uint8 tensor of at least qgemm_moe_sort_workspace(...) bytes,
+    allocated here if not given."""
+    tokens, top_k = _choices(ids, "ids")
+    device, L = ids.device, lib()
+    if isinstance(experts, bool) or not isinstance(experts, int) or not 1 <= experts <= 1024:
+        raise ValueError(f"experts={experts}: need 1 to 1024")
+    slots = tokens * top_k
+    if offsets is None:
+        offsets = _new(experts + 1, _I32, device, stream)
+    if order is None:
+        order = _new(slots, _I32, device, stream)
+    if position is None:
+        position = _new((tokens, top_k), _I32, device, stream)
+    po, pr, pp = (_vec(t, n, size, device, (_I32,)) for t, n, size in
+                  ((offsets, "offsets", experts + 1), (order, "order", slots), (position, "position", slots)))
+    pw = nbytes = 0
+    if workspace is None:
+        nbytes = L.qgemm_moe_sort_workspace(tokens, top_k, experts)
+        if nbytes > 0:
+            # let go here, it goes back to the stream that uses it
+            workspace = _new(nbytes, torch.uint8, device, stream, returned=False)
+            pw = workspace.data_ptr()
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    else:
+        pw, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _enqueue(L.qgemm_moe_sort, device, stream, ids.data_ptr(), tokens, top_k, experts, po, pr, pp, pw or None, nbytes)
+    return offsets, order, position
+
+
+def _token_rows(t, name, tokens, device):
+    shape, ld = _rows(t, name)
+    if shape[0] != tokens or t.device != device:
+        raise ValueError(f"{name} must have {tokens} rows on {device}, got {tuple(shape)} on {t.device}")
+    return shape[1], ld
+
+
+def qgemm_moe_gather(X, position, rows=None, out=None, stream=None):
+    """Each token's row to the rows of its choices: out[position[t, j]] = X[t].
+    X bf16 [tokens, H], position int32 [tokens, top_k] -> bf16 [rows, H] (rows:
+    tokens * top_k unless given); rows that no slot takes are left as they
+    are."""
+    tokens, top_k = _choices(position, "position")
+    device = position.device
+    H, ldx = _token_rows(X, "X", tokens, device)
+    if out is not None:
+        rows = _rows(out, "out", (torch.bfloat16,))[0][0] if rows is None else rows
+    out, ldo = _out_rows(out, "out", (tokens * top_k if rows is None else rows, H), device, stream)
+    _enqueue(lib().qgemm_moe_gather, device, stream, X.data_ptr(), ldx, position.data_ptr(), out.data_ptr(), ldo,
+             tokens, top_k, out.shape[0], H)
+    return out
+
+
+def qgemm_moe_combine(Y, position, weights=None, residual=None, out=None, stream=None):
+    """The rows of each token's choices, summed: out[t] = residual[t] + sum_j
+    weights[t, j] * Y[position[t, j]].  Y bf16 [rows, H], position int32
+    [tokens, top_k], weights fp32 [tokens, top_k] (ones if None), residual bf16
+    [tokens, H] (zeros if None; may be out) -> bf16 [tokens, H].  With neither
+    it is the gradient of qgemm_moe_gather."""
+    tokens, top_k = _choices(position, "position")
+    device = position.device
+    (rows, H), ldy = _rows(Y, "Y")
+    if Y.device != device:
+        raise ValueError(f"Y must be on {device}, found on {Y.device}")
+    pw = None if weights is None else _vec(weights, "weights", tokens * top_k, device, _F32)
+    pr = ldr = 0
+    if residual is not None:
+        rH, ldr = _token_rows(residual, "residual", tokens, device)
+        if rH != H:
+            raise ValueError(f"residual must be [{tokens}, {H}], got [{tokens}, {rH}]")
+        pr = residual.data_ptr()
+    out, ldo = _out_rows(out, "out", (tokens, H), device, stream)
+    _enqueue(lib().qgemm_moe_combine, device, stream, Y.data_ptr(), ldy, position.data_ptr(), pw, pr or None, ldr,
+             out.data_ptr(), ldo, tokens, top_k, rows, H)
+    return out
+
+
+def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, stream=None):
+    """The gradient of qgemm_moe_combine: (dY bf16 [rows, H], dY[position[t, j]]
+    = weights[t, j] * dout[t]; dweights fp32 [tokens, top_k], the product of
+    dout[t] and Y[position[t, j]]).  Rows of dY that no slot takes are left as
+    they are; dY may be Y.  The residual's gradient is dout."""
+    tokens, top_k = _choices(position, "position")
+    device = position.device
+    H, ldd = _token_rows(dout, "dout", tokens, device)
+    (rows, yH), ldy = _rows(Y, "Y")
+    if yH != H or Y.device != device:
+        raise ValueError(f"Y must be [rows, {H}] on {device}, got {tuple(Y.shape)} on {Y.device}")
+    pw = _vec(weights, "weights", tokens * top_k, device, _F32)
+    dY, ldg = _out_rows(dY, "dY", (rows, H), device, stream)
+    if dweights is None:
+        dweights = _new((tokens, top_k), torch.float32, device, stream)
+    _enqueue(lib().qgemm_moe_combine_grad, device, stream, dout.data_ptr(), ldd, Y.data_ptr(), ldy,
+             position.data_ptr(), pw, dY.data_ptr(), ldg, _vec(dweights, "dweights", tokens * top_k, device, _F32),
+             tokens, top_k, rows, H)
+    return dY, dweights
+
+
+# ------------------------------------------------------------ SwiGLU
+
+def _swiglu(entry, first, per_byte, part, dtype, sdtype, X, count, out, scale, stream):
+    """part: elements a scale covers, 0 for the row."""
+    (M, wide), ldx = _rows(X, "X")
+    I = wide // 2
+    if wide % 2 or I % (part or 32):
+        raise ValueError(f"X is [M, {wide}]: need two halves, each a multiple of {part or 32}")
+    device = X.device
+    pc = None if count is None else _vec(count, "count", 1, device, (_I32,))
+    out, ldq = _norm_codes(out, M, I // per_byte, device, dtype, stream)
+    if not part:
+        scale = _new(M, sdtype, device, stream) if scale is None else scale
+        tail = (_vec(scale, "scale", M, device, (sdtype,)),)
+    else:
+        if scale is None:
+            scale = _new((M, I // part), sdtype, device, stream)
+        sshape, lds = _rows(scale, "scale", (sdtype,))
+        if tuple(sshape) != (M, I // part) or scale.device != device:
+            raise ValueError(f"scale must be {sdtype} [{M}, {I // part}] on {device}")
+        tail = (scale.data_ptr(), lds)
+    _enqueue(entry, device, stream, *first, X.data_ptr(), ldx, pc, out.data_ptr(), ldq, *tail, M, I)
+    return out, scale
+
+
+def qgemm_swiglu_quant_i8_rowwise(X, count=None, out=None, scale=None, stream=None):
+    """silu(g) * u of X = [g | u], bf16 [M, 2 I] -> (int8 codes [M, I], scale
+    fp32 [M]): the A operand and scale_a of qgemm_i8_rowwise and its grouped
+    form.  count: int32 GPU tensor of one element (such as offsets[-1:] of the
+    sort): rows from there on are left as they are."""
+    return _swiglu(lib().qgemm_swiglu_quant_i8_rowwise, (), 1, 0, torch.int8, torch.float32, X, count, out, scale,
+                   stream)
+
+
+def qgemm_swiglu_quant_f8_pertoken(X, count=None, out=None, scale=None, stream=None):
+    """silu(g) * u of X = [g | u] -> (e4m3 codes as uint8 [M, I], scale fp32
+    [M]): the A operand and scale_a of qgemm_f8_pertoken and its grouped form;
+    count as for the int8 form."""
+    return _swiglu(lib().qgemm_swiglu_quant_f8_pertoken, (), 1, 0, torch.uint8, torch.float32, X, count, out, scale,
+                   stream)
+
+
+def qgemm_swiglu_quant_f8_block(X, count=None, out=None, scale=None, stream=None):
+    """silu(g) * u of X = [g | u] -> (e4m3 codes as uint8 [M, I], scales fp32
+    [M, I/128]): the A operand and scale_a of qgemm_f8_blockscale and its
+    grouped form.  I a multiple of 128."""
+    return _swiglu(lib().qgemm_swiglu_quant_f8_block, (), 1, 128, torch.uint8, torch.float32, X, count, out, scale,
+                   stream)
+
+
+def qgemm_swiglu_quant_mx(fmt, X, count=None, out=None, scale=None, stream=None):
+    """silu(g) * u of X = [g | u] -> (codes uint8 [M, I] (e4m3) or [M, I/2]
+    (e2m1), ue8m0 scales uint8 [M, I/32]): the A operand and scale_a of qgemm_mx
+    and its grouped form."""
+    if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
+        raise ValueError(f"unknown MX format {fmt}")
+    return _swiglu(lib().qgemm_swiglu_quant_mx, (fmt,), 1 if fmt == QGEMM_MX_E4M3 else 2, 32, torch.uint8, torch.uint8,
+                   X, count, out, scale, stream)
+
+
+# ------------------------------------------------------------ grouped GEMMs
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_UE8M0 = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+
+
+def _table(t, name, shape, dtypes, device):
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be {dtypes} {tuple(shape)}, contiguous, on {device}")
+    return t.data_ptr()
+
+
+def _grouped(entry, first, dtypes, per_byte, sdtypes, sa_shape, sb_shape, A, B, scale_a, scale_b, offsets, order, top_k,
+             bias, out, stream):
+    """sa_shape, sb_shape: of the scales, from (rows, K) and (experts, N, K)."""
+    (a_rows, row), lda = _rows(A, "A", dtypes)
+    device = A.device
+    if not isinstance(B, torch.Tensor) or B.dtype not in dtypes or B.device != device or B.dim() != 3:
+        raise ValueError(f"B must be a tensor of {dtypes} [experts, N, K] on {device}")
+    experts, N, brow = B.shape
+    sb, ldb = B.stride(), B.stride(1) if N > 1 else brow
+    if brow != row:
+        raise ValueError(f"A has rows of {row} bytes, B of {brow}")
+    if (brow > 1 and sb[2] != 1) or (experts > 1 and sb[0] != N * ldb):
+        raise ValueError("B must have unit stride along K and its experts N rows apart")
+    K = row * per_byte
+    if not isinstance(top_k, int) or top_k < 1:
+        raise ValueError(f"top_k={top_k}: need at least 1")
+    if not isinstance(offsets, torch.Tensor) or offsets.numel() != experts + 1:
+        raise ValueError(f"offsets must hold {experts + 1} values")
+    po = _vec(offsets, "offsets", experts + 1, device, (_I32,))
+    if order is None:
+        rows, pr = a_rows, None
+    else:
+        if not isinstance(order, torch.Tensor) or order.dim() != 1:
+            raise ValueError("order must be a 1-D tensor")
+        rows = order.shape[0]
+        pr = _vec(order, "order", rows, device, (_I32,))
+    psa = _table(scale_a, "scale_a", sa_shape(a_rows, K), sdtypes, device)
+    psb = _table(scale_b, "scale_b", sb_shape(experts, N, K), sdtypes, device)
+    pb = None if bias is None else _table(bias, "bias", (experts, N), _BF16, device)
+    if out is None:
+        wide = N + (-N) % 8                   # the library's rule for row strides
+        out, ldc = _new((rows, wide), torch.bfloat16, device, stream), wide
+        out = out if wide == N else out[:, :N]
+    else:
+        out, ldc = _out_rows(out, "out", (rows, N), device, stream)
+        ldc = ldc if rows > 1 else N + (-N) % 8
+    _enqueue(entry, device, stream, *first, A.data_ptr(), lda if a_rows > 1 else row, a_rows, B.data_ptr(), ldb, psa,
+             psb, po, pr, top_k, pb, out.data_ptr(), ldc, rows, experts, N, K)
+    return out
+
+
+def _row_a(rows, K):
+    return (rows,)
+
+
+def _row_b(experts, N, K):
+    return (experts, N)
+
+
+def qgemm_i8_rowwise_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+    """One qgemm_i8_rowwise per expert over its rows: rows offsets[e] ..
+    offsets[e+1]-1 of the result are rows of A times B[e].  With an order (of
+    the sort) A holds the tokens and row r takes token order[r] // top_k; without
+    one A holds the rows.  A int8 [rows of A, K], B int8 [experts, N, K], scale_a
+    fp32 [rows of A], scale_b fp32 [experts, N], bias bf16 [experts, N] -> bf16
+    [rows, N]; rows past offsets[experts] are left as they are.  K a multiple of
+    128."""
+    return _grouped(lib().qgemm_i8_rowwise_grouped, (), (torch.int8,), 1, _F32, _row_a, _row_b, A, B, scale_a, scale_b,
+                    offsets, order, top_k, bias, out, stream)
+
+
+def qgemm_f8_pertoken_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+    """One qgemm_f8_pertoken per expert over its rows; A, B e4m3 (uint8 or
+    float8_e4m3fn), otherwise as qgemm_i8_rowwise_grouped."""
+    return _grouped(lib().qgemm_f8_pertoken_grouped, (), _E4M3, 1, _F32, _row_a, _row_b, A, B, scale_a, scale_b,
+                    offsets, order, top_k, bias, out, stream)
+
+
+def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None,
+                                stream=None):
+    """One qgemm_f8_blockscale per expert over its rows; scale_a fp32
+    [rows of A, K/128], scale_b fp32 [experts, ceil(N/128), K/128], otherwise as
+    qgemm_f8_pertoken_grouped."""
+    return _grouped(lib().qgemm_f8_blockscale_grouped, (), _E4M3, 1, _F32, lambda m, k: (m, k // 128),
+                    lambda e, n, k: (e, -(-n // 128), k // 128), A, B, scale_a, scale_b, offsets, order, top_k, bias,
+                    out, stream)
+
+
+def qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+    """One qgemm_mx per expert over its rows; A, B e4m3 or e2m1 (two codes a
+    byte, rows of K/2 bytes), scale_a ue8m0 [rows of A, K/32], scale_b ue8m0
+    [experts, N, K/32], otherwise as qgemm_i8_rowwise_grouped."""
+    if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
+        raise ValueError(f"unknown MX format {fmt}")
+    wide = fmt == QGEMM_MX_E4M3
+    return _grouped(lib().qgemm_mx_grouped, (fmt,), _E4M3 if wide else (torch.uint8,), 1 if wide else 2, _UE8M0,
+                    lambda m, k: (m, k // 32), lambda e, n, k: (e, n, k // 32), A, B, scale_a, scale_b, offsets, order,
+                    top_k, bias, out, stream)

@@ -175,6 +175,85 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
                        torch.uint8, X, gamma, eps, residual, residual_out, out, scale, stream)
 
 
+# ------------------------------------------------------------ norms after and before a block
+
+class _Postnorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("Y", "R", "gamma_post", "gate", "gamma", "Rout")] + \
+        [(n, ctypes.c_int64) for n in ("ldy", "ldr", "ldo")] + [("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
+
+
+def _postnorm(entry, first, per_byte, part, dtype, sdtype, Y, residual, gamma_post, gamma, eps, gate, alpha,
+              residual_out, out, scale, stream):
+    """part: elements a scale covers, 0 for the row."""
+    shape, ldy = _rows(Y, "Y")
+    device = Y.device
+    M, K = shape
+    if K % (part or 32):
+        raise ValueError(f"K={K} is not a multiple of {part or 32}")
+    rshape, ldr = _rows(residual, "residual")
+    if rshape != shape or residual.device != device:
+        raise ValueError(f"residual must be {tuple(shape)} on {device}, got {tuple(rshape)} on {residual.device}")
+    if residual_out is None:
+        residual_out, ldo = _new(shape, torch.bfloat16, device, stream), K
+    else:
+        oshape, ldo = _rows(residual_out, "residual_out")
+        if oshape != shape or residual_out.device != device:
+            raise ValueError(f"residual_out must be {tuple(shape)} on {device}, got {tuple(oshape)} on "
+                             f"{residual_out.device}")
+    out, ldq = _norm_codes(out, M, K // per_byte, device, dtype, stream)
+    if not part:
+        scale = _new(M, sdtype, device, stream) if scale is None else scale
+        tail = (_vec(scale, "scale", M, device, (sdtype,)),)
+    else:
+        if scale is None:
+            scale = _new((M, K // part), sdtype, device, stream)
+        sshape, lds = _rows(scale, "scale", (sdtype,))
+        if tuple(sshape) != (M, K // part) or scale.device != device:
+            raise ValueError(f"scale must be {sdtype} [{M}, {K // part}] on {device}")
+        tail = (scale.data_ptr(), lds)
+    norm = _Postnorm(Y.data_ptr(), residual.data_ptr(), _vec(gamma_post, "gamma_post", K, device),
+                     None if gate is None else _vec(gate, "gate", K, device), _vec(gamma, "gamma", K, device),
+                     residual_out.data_ptr(), ldy, ldr, ldo, eps, alpha)
+    _enqueue(entry, device, stream, *first, ctypes.addressof(norm), out.data_ptr(), ldq, *tail, M, K)
+    return out, scale, residual_out
+
+
+def qgemm_postnorm_quant_i8_rowwise(Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None,
+                                    out=None, scale=None, stream=None):
+    """The end of a block and the beginning of the next: h = residual + alpha *
+    gate * rmsnorm(Y; gamma_post), then the RMS norm of h with gamma -> (int8
+    codes [M, K], scale fp32 [M], h in bf16).  Y, residual bf16 [M, K];
+    gamma_post, gamma, gate (ones if None) bf16 [K]; residual_out may be
+    residual itself."""
+    return _postnorm(lib().qgemm_postnorm_quant_i8_rowwise, (), 1, 0, torch.int8, torch.float32, Y, residual,
+                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+
+
+def qgemm_postnorm_quant_f8_pertoken(Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0,
+                                     residual_out=None, out=None, scale=None, stream=None):
+    """The same -> (e4m3 codes as uint8 [M, K], scale fp32 [M], h in bf16)."""
+    return _postnorm(lib().qgemm_postnorm_quant_f8_pertoken, (), 1, 0, torch.uint8, torch.float32, Y, residual,
+                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+
+
+def qgemm_postnorm_quant_f8_block(Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None,
+                                  out=None, scale=None, stream=None):
+    """The same -> (e4m3 codes as uint8 [M, K], scales fp32 [M, K/128], h in
+    bf16).  K a multiple of 128."""
+    return _postnorm(lib().qgemm_postnorm_quant_f8_block, (), 1, 128, torch.uint8, torch.float32, Y, residual,
+                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+
+
+def qgemm_postnorm_quant_mx(fmt, Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None,
+                            out=None, scale=None, stream=None):
+    """The same -> (codes uint8 [M, K] (e4m3) or [M, K/2] (e2m1), ue8m0 scales
+    uint8 [M, K/32], h in bf16)."""
+    if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
+        raise ValueError(f"unknown MX format {fmt}")
+    return _postnorm(lib().qgemm_postnorm_quant_mx, (fmt,), 1 if fmt == QGEMM_MX_E4M3 else 2, 32, torch.uint8,
+                     torch.uint8, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+
+
 # ------------------------------------------------------------ 8-bit cache
 
 class _CacheStruct(ctypes.Structure):

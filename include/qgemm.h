@@ -503,6 +503,151 @@ qgemm_status qgemm_w4_matvec_mx(const uint16_t *X, int64_t ldx, const uint8_t *W
                                 const uint8_t *scale_b, qgemm_mx_bscale b_layout, const uint16_t *bias, uint16_t *Y,
                                 int64_t ldy, int64_t M, int64_t N, int64_t K, void *stream);
 
+/* The end of a block and the beginning of the next in one pass: the norm after
+ * the block, its gate and residual scale, and the norm before the next block
+ * with quantised output.  Per row m, in binary32:
+ *   n    = Y * 1/sqrt(mean(Y^2) + eps) * gamma_post
+ *   h    = R + alpha * (n * gate)      (n where gate is NULL)
+ *   Rout = bf16(h)                     (not written where Rout is NULL)
+ *   z    = (h * gamma) * 1/sqrt(mean(h^2) + eps)
+ *   Q, scales = the quantiser's rule on z, as for the norms above
+ * The struct is host memory read during the call:
+ *   Y      [M, K] bf16, the block's output, row stride ldy ELEMENTS (multiple
+ *          of 8)
+ *   R      [M, K] bf16, the residual stream, row stride ldr
+ *   Rout   [M, K] bf16 or NULL, row stride ldo; may be R or Y itself (same
+ *          pointer and stride), otherwise disjoint
+ *   gamma_post, gamma  [K] bf16;  gate  [K] bf16 or NULL
+ *   eps    >= 0;  alpha finite
+ * Q, ldq, scale / S, lds, M, K, alignment and what is not finite: as for the
+ * norms above. */
+typedef struct {
+    const uint16_t *Y;
+    const uint16_t *R;
+    const uint16_t *gamma_post;
+    const uint16_t *gate;
+    const uint16_t *gamma;
+    uint16_t *Rout;
+    int64_t ldy;
+    int64_t ldr;
+    int64_t ldo;
+    float eps;
+    float alpha;
+} qgemm_postnorm;
+qgemm_status qgemm_postnorm_quant_i8_rowwise(const qgemm_postnorm *norm, int8_t *Q, int64_t ldq, float *scale,
+                                             int64_t M, int64_t K, void *stream);
+qgemm_status qgemm_postnorm_quant_f8_pertoken(const qgemm_postnorm *norm, uint8_t *Q, int64_t ldq, float *scale,
+                                              int64_t M, int64_t K, void *stream);
+qgemm_status qgemm_postnorm_quant_f8_block(const qgemm_postnorm *norm, uint8_t *Q, int64_t ldq, float *S, int64_t lds,
+                                           int64_t M, int64_t K, void *stream);
+qgemm_status qgemm_postnorm_quant_mx(qgemm_mx_fmt fmt, const qgemm_postnorm *norm, void *Q, int64_t ldq, uint8_t *S,
+                                     int64_t lds, int64_t M, int64_t K, void *stream);
+
+/* ---------------------------------------------------------------------
+ * A layer of experts: each token goes through top_k of them.  A choice (slot)
+ * is one token's j-th expert, slot = token * top_k + j.  Conventions as above
+ * (device memory of the caller, asynchronous on the stream, nothing allocated).
+ * --------------------------------------------------------------------- */
+
+/* The choices in order of experts, stable: rows offsets[e] .. offsets[e+1]-1
+ * are expert e's, by slot.
+ *   ids       [tokens, top_k] int32; a slot whose id lies outside
+ *             [0, experts) has no row (another rank's expert, padding)
+ *   offsets   [experts + 1] int32
+ *   order     [tokens * top_k] int32: the slot of each row; -1 from
+ *             offsets[experts] on
+ *   position  [tokens, top_k] int32: the row of each slot; -1 without one
+ *   workspace qgemm_moe_sort_workspace(...) bytes, 16-byte aligned (may be NULL
+ *             if that is 0); contents undefined before and after; one call at
+ *             a time
+ * experts 1 to 1024, top_k 1 to 64, tokens * top_k < 2^30; tokens == 0 gives
+ * offsets of zero. */
+int64_t qgemm_moe_sort_workspace(int64_t tokens, int64_t top_k, int64_t experts);
+qgemm_status qgemm_moe_sort(const int32_t *ids, int64_t tokens, int64_t top_k, int64_t experts, int32_t *offsets,
+                            int32_t *order, int32_t *position, void *workspace, int64_t workspace_bytes,
+                            void *stream);
+
+/* Tokens' rows to their experts and back.  position as the sort gives it: rows
+ * in [0, rows), each at most once; anything else stands for no expert.
+ *   gather    Y[position[t,j]] = X[t]; rows that no slot takes keep their bytes
+ *   combine   O[t] = bf16( R[t] + sum_j weights[t,j] * Y[position[t,j]] ), the
+ *             sum in binary32 in the order of j; R NULL: zeros; weights NULL:
+ *             ones.  Without either it is the gather's gradient.
+ *   gradient  dY[position[t,j]] = bf16( weights[t,j] * dO[t] ),
+ *             dweights[t,j] = sum_h dO[t,h] * Y[position[t,j],h] in binary32, 0
+ *             without an expert; rows of dY that no slot takes keep their bytes
+ *   X, O, R, dO   [tokens, H] bf16, row strides in ELEMENTS (multiples of 8)
+ *   Y, dY         [rows, H] bf16; dY may be Y itself
+ *   weights, dweights   [tokens, top_k] fp32
+ * O may be R itself.  H a positive multiple of 8; 16-byte aligned rows.  A slot
+ * without an expert adds nothing, whatever its weight is. */
+qgemm_status qgemm_moe_gather(const uint16_t *X, int64_t ldx, const int32_t *position, uint16_t *Y, int64_t ldy,
+                              int64_t tokens, int64_t top_k, int64_t rows, int64_t H, void *stream);
+qgemm_status qgemm_moe_combine(const uint16_t *Y, int64_t ldy, const int32_t *position, const float *weights,
+                               const uint16_t *R, int64_t ldr, uint16_t *O, int64_t ldo, int64_t tokens,
+                               int64_t top_k, int64_t rows, int64_t H, void *stream);
+qgemm_status qgemm_moe_combine_grad(const uint16_t *dO, int64_t lddo, const uint16_t *Y, int64_t ldy,
+                                    const int32_t *position, const float *weights, uint16_t *dY, int64_t lddy,
+                                    float *dweights, int64_t tokens, int64_t top_k, int64_t rows, int64_t H,
+                                    void *stream);
+
+/* silu(g) * u of X = [g | u] with quantised output: the A operand and scales of
+ * the product that follows.  y = g / (1 + exp(-g)) * u in binary32, then the
+ * quantiser's rule as for the norms above (i8_rowwise, f8_pertoken, f8_block,
+ * mx); y itself is within a few units in the last place of binary32.
+ *   X      [M, 2 I] bf16, row stride ldx ELEMENTS (multiple of 8)
+ *   count  NULL, or one int32 on the device: rows from there on are left as
+ *          they are in Q and the scales (offsets + experts of the sort)
+ *   Q, ldq, scale / S, lds   as for the norms, for rows of I elements
+ * I a positive multiple of 32 (f8_block: 128); X, Q 16-byte aligned.  What is
+ * not finite shows in the scales, as for the norms. */
+qgemm_status qgemm_swiglu_quant_i8_rowwise(const uint16_t *X, int64_t ldx, const int32_t *count, int8_t *Q,
+                                           int64_t ldq, float *scale, int64_t M, int64_t I, void *stream);
+qgemm_status qgemm_swiglu_quant_f8_pertoken(const uint16_t *X, int64_t ldx, const int32_t *count, uint8_t *Q,
+                                            int64_t ldq, float *scale, int64_t M, int64_t I, void *stream);
+qgemm_status qgemm_swiglu_quant_f8_block(const uint16_t *X, int64_t ldx, const int32_t *count, uint8_t *Q,
+                                         int64_t ldq, float *S, int64_t lds, int64_t M, int64_t I, void *stream);
+qgemm_status qgemm_swiglu_quant_mx(qgemm_mx_fmt fmt, const uint16_t *X, int64_t ldx, const int32_t *count, void *Q,
+                                   int64_t ldq, uint8_t *S, int64_t lds, int64_t M, int64_t I, void *stream);
+
+/* One scaled product per expert over its rows:
+ *   C[r,n] = the GEMM of the same name on row a(r) of A and B[e],
+ *            offsets[e] <= r < offsets[e+1]
+ *   a(r) = order[r] / top_k with an order (A holds the tokens), r without one
+ *          (A holds the rows)
+ *   A        [a_rows, K] codes, row stride lda bytes (multiple of 16)
+ *   B        [experts, N, K] codes, row stride ldb bytes (multiple of 16), the
+ *            experts N * ldb apart
+ *   scale_a  as the GEMM's, for a_rows rows
+ *   scale_b  [experts, N] fp32 (i8, f8_pertoken); [experts, ceil(N/128), K/128]
+ *            fp32 (f8_blockscale); [experts, N, K/32] (mx)
+ *   bias     [experts, N] bf16 or NULL
+ *   C        [rows, ldc] bf16; rows at or past offsets[experts] keep their bytes
+ *   offsets  [experts + 1], order [rows], as the sort gives them
+ * K a positive multiple of 128 (i8: at most 131071); with an order a_rows * lda
+ * below 2^31; block and MX scales 16-byte aligned; else as for the GEMMs.  fmt
+ * e4m3 or e2m1.  Offsets outside [0, rows] are clamped; a row whose token A does
+ * not have takes zeros (and scale zero).  Sums are exact (i8) or binary32 in an
+ * order that depends on the arguments' sizes alone. */
+qgemm_status qgemm_i8_rowwise_grouped(const int8_t *A, int64_t lda, int64_t a_rows, const int8_t *B, int64_t ldb,
+                                      const float *scale_a, const float *scale_b, const int32_t *offsets,
+                                      const int32_t *order, int64_t top_k, const uint16_t *bias, uint16_t *C,
+                                      int64_t ldc, int64_t rows, int64_t experts, int64_t N, int64_t K, void *stream);
+qgemm_status qgemm_f8_pertoken_grouped(const uint8_t *A, int64_t lda, int64_t a_rows, const uint8_t *B, int64_t ldb,
+                                       const float *scale_a, const float *scale_b, const int32_t *offsets,
+                                       const int32_t *order, int64_t top_k, const uint16_t *bias, uint16_t *C,
+                                       int64_t ldc, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                       void *stream);
+qgemm_status qgemm_f8_blockscale_grouped(const uint8_t *A, int64_t lda, int64_t a_rows, const uint8_t *B, int64_t ldb,
+                                         const float *scale_a, const float *scale_b, const int32_t *offsets,
+                                         const int32_t *order, int64_t top_k, const uint16_t *bias, uint16_t *C,
+                                         int64_t ldc, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                         void *stream);
+qgemm_status qgemm_mx_grouped(qgemm_mx_fmt fmt, const void *A, int64_t lda, int64_t a_rows, const void *B, int64_t ldb,
+                              const uint8_t *scale_a, const uint8_t *scale_b, const int32_t *offsets,
+                              const int32_t *order, int64_t top_k, const uint16_t *bias, uint16_t *C, int64_t ldc,
+                              int64_t rows, int64_t experts, int64_t N, int64_t K, void *stream);
+
 /* Text of the last non-OK status returned on the calling thread ("" if none). */
 const char *qgemm_last_error(void);
 
