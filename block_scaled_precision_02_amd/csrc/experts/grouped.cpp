@@ -8,25 +8,50 @@ namespace qgemm {
 
 namespace {
 
-// The tile by the rows an expert has on average (how they are spread is known
-// on the device alone).
+// The tile by what the host knows: the rows an expert has on average (how they
+// are spread is known on the device alone) and the most experts that can have
+// any.  One MI355X, us, experts chosen at random, some more often; 8 of 64
+// experts or as said:
+//  * Above 160 rows an expert the 256-row tiles, bound by the matrix cores
+//    (XXX).
+//  * Above 16 the 128x128 tile (512 tokens, 4096x4096: i8 271, panel 296; e2m1
+//    153 and 182).
+//  * Up to 16 rows the weights' bytes are all that counts, and a chip full of
+//    loads: the panel where it has two workgroups a CU (64 tokens, 256 experts,
+//    2048x7168: blockscale 418, 128x128 451, stream 572; 16 tokens, 128
+//    experts, 4096x7168: e4m3 MX 363, 409 and 350).
+//  * Fewer workgroups: the stream, whose waves each take 16 columns (3 tokens,
+//    2112x7168: e4m3 MX 67, panel 82, 128x128 87; one token, 2048x7168: i8 23,
+//    35 and 39) while an expert's rows are one tile of it mostly; else the
+//    128x128 tile (10 tokens, 8 experts, 4096x4096: 35 for all three).
+//  * So few columns that a wave over K would be the whole time: the small-M
+//    kernel, eight waves over K (one token, 512x7168: i8 10.5, stream 20, 128x128
+//    24; 1024x7168: 19, 20 and 25).
 int pick_tile(int path, const GroupedArgs &a)
 {
     const int64_t each = (a.rows + a.experts - 1) / a.experts;
-    if (each <= 16)
-        return SKINNY16_TILE;
-    if (each <= 160)
+    if (each > 160)
+        return path == PATH_F8B ? F8B256_TILE : DMA8_TILE;
+    if (each > 16)
         return DMA128_TILE;
-    return path == PATH_F8B ? F8B256_TILE : DMA8_TILE;
+    const int64_t panels = std::min<int64_t>(a.rows, a.experts) * ((a.N + PANEL_BN - 1) / PANEL_BN);
+    if (panels <= 64)
+        return SKINNY16_TILE;
+    if (panels >= 512)
+        return PANEL64_TILE;
+    return each <= 4 ? STREAM16_TILE : DMA128_TILE;
 }
+
+int edge_m(int tile) { return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? 64 : tile_edge_m(tile); }
+int edge_n(int tile) { return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? PANEL_BN : tile_edge_n(tile); }
 
 // The most row tiles there can be: one partly filled for each expert with rows.
 int64_t most_tiles_m(int tile, const GroupedArgs &a)
 {
-    return a.rows / tile_edge_m(tile) + std::min<int64_t>(a.rows, a.experts);
+    return a.rows / edge_m(tile) + std::min<int64_t>(a.rows, a.experts);
 }
 
-int64_t tiles_n(int tile, const GroupedArgs &a) { return ((int64_t)a.N + tile_edge_n(tile) - 1) / tile_edge_n(tile); }
+int64_t tiles_n(int tile, const GroupedArgs &a) { return ((int64_t)a.N + edge_n(tile) - 1) / edge_n(tile); }
 
 }  // namespace
 

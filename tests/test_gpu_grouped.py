@@ -138,7 +138,8 @@ def test_sizes(kind, counts, N, K, top_k):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("rows,experts,N,K", [(60, 200, 272, 256), (500, 70, 136, 896), (3000, 24, 520, 384),
-                                              (5000, 12, 264, 1280), (900, 1, 1024, 256), (2000, 1024, 48, 128)])
+                                              (5000, 12, 264, 1280), (900, 1, 1024, 256), (2000, 1024, 48, 128),
+                                              (300, 64, 1100, 640), (700, 60, 1161, 384)])
 def test_uneven(kind, rows, experts, N, K):
     for top_k in (0, 8):
         c = Case(kind, spread(rows, experts, rows), N, K, top_k, seed=rows)
@@ -151,6 +152,18 @@ def test_uneven(kind, rows, experts, N, K):
 def test_odd_columns(kind, N, each):
     c = Case(kind, [each, 1, each], N, 256, 2, bias=True, seed=N)
     c.check(c.call())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("experts,N", [(300, 129), (200, 385), (64, 1030), (7, 1537)])
+def test_odd_columns_of_few_rows(kind, experts, N):
+    """64-row panels and the stream of single waves."""
+    for K in (128, 896):
+        c = Case(kind, spread(2 * experts, experts, N), N, K, 2, bias=True, extra=3, seed=N)
+        out = torch.full((c.rows, N + (-N) % 8), 9.0, dtype=torch.bfloat16, device="cuda")
+        c.call(out=out[:, :N])
+        c.check(out[:, :N])
+        assert bool((out[:, N:] == 9).all()) and bool((out[2 * experts:] == 9).all())
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -176,11 +189,11 @@ def test_rows_behind_the_last_and_strides(kind, each):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("each", [4, 80, 280])
-def test_broken_offsets_and_orders_stay_in_range(kind, each):
+@pytest.mark.parametrize("each,N", [(4, 128), (80, 128), (280, 128), (4, 16384), (4, 4096)])
+def test_broken_offsets_and_orders_stay_in_range(kind, each, N):
     """Offsets outside the rows are clamped, tokens that are not there are zeros:
     nothing else is written."""
-    c = Case(kind, [each] * 4, 128, 256, 2, extra=10, seed=each)
+    c = Case(kind, [each] * 4, N, 256, 2, extra=10, seed=each)
     want = c.call()
     live = 4 * each
     c.order[3] = -1
@@ -192,7 +205,7 @@ def test_broken_offsets_and_orders_stay_in_range(kind, each):
     for values in ([-5, each, 2 * each, 3 * each, 10 ** 9], [0, 0, 0, 0, 0], [7, 3, 2, 1, 0], [2 ** 31 - 1] * 5,
                    [-2 ** 31] * 5):
         c.offsets = torch.tensor(values, dtype=torch.int32, device="cuda")
-        buf = torch.full((c.rows + 64, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+        buf = torch.full((c.rows + 64, N), 9.0, dtype=torch.bfloat16, device="cuda")
         c.call(out=buf[:c.rows])
         assert bool((buf[c.rows:] == 9).all())
         if values[0] == -5:
@@ -204,14 +217,16 @@ def test_broken_offsets_and_orders_stay_in_range(kind, each):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_a_row_has_the_same_bits_wherever_it_stands(kind):
+@pytest.mark.parametrize("counts,N", [([70, 90, 100], 320), ([2, 70, 0, 13, 1] * 10, 1290), ([1, 3, 2], 2100),
+                                      ([300, 200], 512)])
+def test_a_row_has_the_same_bits_wherever_it_stands(kind, counts, N):
     """The sums' order is the sizes' alone: not the row's place, the expert's
     other rows, or the way its token is found."""
-    c = Case(kind, [70, 90, 100], 320, 512, 0, seed=8)
+    c = Case(kind, counts, N, 512, 0, seed=8)
     out = c.call()
     assert torch.equal(out, c.call())
     back = torch.arange(c.rows, device="cuda").flip(0)
-    c2 = Case(kind, [100, 90, 70], 320, 512, 0, seed=8)
+    c2 = Case(kind, counts[::-1], N, 512, 0, seed=8)
     c2.a, c2.sa, c2.b, c2.sb = c.a, c.sa, c.b.flip(0).contiguous(), c.sb.flip(0).contiguous()
     c2.order, c2.top_k = back.int().contiguous(), 1
     assert torch.equal(c2.call().flip(0), out)
@@ -252,7 +267,9 @@ def test_same_bits_as_the_dense_gemm(kind, counts, N, K):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("counts,N,K", [([3, 0, 17], 136, 896), ([100, 3, 250], 264, 640), ([600, 1, 300], 392, 512)])
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 17], 136, 896), ([100, 3, 250], 264, 640), ([600, 1, 300], 392, 512),
+                                        (([30, 0, 1, 16] * 16), 1300, 640), ([5] * 9 + [0] * 20, 1312, 1152),
+                                        ([1] * 8, 2056, 384)])
 @pytest.mark.parametrize("top_k", [0, 2])
 def test_exact_sums(kind, counts, N, K, top_k):
     """Small whole numbers under powers of two: every sum is exact in binary32,
@@ -301,23 +318,23 @@ def test_weights_past_4_gib(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("each", [3, 100, 300])
-def test_streams_and_graph(kind, each):
-    c = Case(kind, [each, 2 * each], 256, 256, 2, seed=2)
+@pytest.mark.parametrize("each,N", [(3, 256), (100, 256), (300, 256), (3, 4096), (3, 40000)])
+def test_streams_and_graph(kind, each, N):
+    c = Case(kind, [each, 2 * each], N, 256, 2, seed=2)
     want = c.call()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     got = c.call(stream=side)
     side.synchronize()
     assert torch.equal(got, want)
-    out = torch.zeros(c.rows, 256, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(c.rows, N, dtype=torch.bfloat16, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         c.call(out=out)
     for i in range(3):
         # other tokens and other counts under the same graph
         c.order.copy_(c.order.roll(7))
-        c.offsets.copy_(torch.tensor([0, each + 10 * i, 3 * each], dtype=torch.int32))
+        c.offsets.copy_(torch.tensor([0, min(each + 10 * i, 3 * each), 3 * each], dtype=torch.int32))
         out.zero_()
         graph.replay()
         torch.cuda.synchronize()
