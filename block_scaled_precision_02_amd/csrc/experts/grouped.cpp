@@ -10,27 +10,29 @@ namespace {
 
 // The tile by what the host knows: the rows an expert has on average (how they
 // are spread is known on the device alone) and the most experts that can have
-// any.  One MI355X, us, experts chosen at random, some more often; 8 of 64
-// experts or as said:
-//  * Above 160 rows an expert the 256-row tiles, bound by the matrix cores
-//    (XXX).
-//  * Above 16 the 128x128 tile (512 tokens, 4096x4096: i8 271, panel 296; e2m1
-//    153 and 182).
+// any.  One MI355X, us, experts chosen at random, some more often:
+//  * Above 96 rows an expert the 256-row tiles, bound by the matrix cores (64
+//    experts of 4096x4096: at 122 rows i8 288 and 337 on 128x128, at 66 rows 267
+//    and 270; e2m1 178 and 187, 161 and 152).  Blockscale, whose 256x128 tile has
+//    one wave a SIMD, from 2048 rows (8 of 4096x4096, 4096 rows: 714 and 749; 64
+//    of 4096x2048, 375 rows: 364 and 354).
+//  * Above 16 the 128x128 tile (64 of 4096x4096, 32 rows: i8 241, panel 247; e2m1
+//    139 and 148).
 //  * Up to 16 rows the weights' bytes are all that counts, and a chip full of
-//    loads: the panel where it has two workgroups a CU (64 tokens, 256 experts,
-//    2048x7168: blockscale 418, 128x128 451, stream 572; 16 tokens, 128
-//    experts, 4096x7168: e4m3 MX 363, 409 and 350).
-//  * Fewer workgroups: the stream, whose waves each take 16 columns (3 tokens,
-//    2112x7168: e4m3 MX 67, panel 82, 128x128 87; one token, 2048x7168: i8 23,
-//    35 and 39) while an expert's rows are one tile of it mostly; else the
-//    128x128 tile (10 tokens, 8 experts, 4096x4096: 35 for all three).
+//    loads: the panel where it has two workgroups a CU (64 tokens, 8 of 256
+//    experts of 2048x7168: blockscale 418, 128x128 451, stream 572; 16 tokens, 8 of
+//    128 of 4096x7168: e4m3 MX 363, 409 and 350).
+//  * Fewer workgroups: the stream, whose waves each take 16 columns (3 tokens, 8
+//    of 64 of 2112x7168: e4m3 MX 67, panel 82, 128x128 87; one token, 2048x7168: i8
+//    23, 35 and 39) while an expert's rows are one tile of it mostly; else the
+//    128x128 tile (10 tokens, 4 of 8 of 4096x4096: 35 for all three).
 //  * So few columns that a wave over K would be the whole time: the small-M
-//    kernel, eight waves over K (one token, 512x7168: i8 10.5, stream 20, 128x128
-//    24; 1024x7168: 19, 20 and 25).
+//    kernel, eight waves over K (one token, 8 of 64 of 512x7168: i8 10.5, stream
+//    20, 128x128 24; 1024x7168: 19, 20 and 25).
 int pick_tile(int path, const GroupedArgs &a)
 {
     const int64_t each = (a.rows + a.experts - 1) / a.experts;
-    if (each > 160)
+    if (each > (path == PATH_F8B ? 2048 : 96))
         return path == PATH_F8B ? F8B256_TILE : DMA8_TILE;
     if (each > 16)
         return DMA128_TILE;

@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(128 * WN, 1)
                 sb_nxt[j] = crb[j][W] >> sh;
         }
     };
-    auto mfmas = [&](auto sc, auto setc, auto q0c, auto q1c, auto jc) {
+    auto mfmas = [&](auto sc, auto setc, auto q0c, auto q1c, auto jc, auto livec) {
         constexpr int S = decltype(sc)::value;
         constexpr int SET = decltype(setc)::value;
         constexpr int J = decltype(jc)::value;
@@ -900,7 +900,8 @@ __global__ void __launch_bounds__(128 * WN, 1)
             constexpr int Q = decltype(qc)::value;
             constexpr int i = Q / TN;
             constexpr int j = (i & 1) ? (TN - 1 - Q % TN) : (Q % TN);
-            if constexpr (BS) {
+            if constexpr (i >= decltype(livec)::value) {
+            } else if constexpr (BS) {
                 if constexpr ((J & 1) == 0) {
                     // first stage of a K block: the partial sum starts at zero
                     pacc[i][j] = Acc{};
@@ -917,8 +918,8 @@ __global__ void __launch_bounds__(128 * WN, 1)
     };
     // Blockscale, a K block's second stage: total += partial * (sa * sb) for
     // the MFMA tile Q of the serpentine order.
-    auto fold = [&](auto qc) {
-        if constexpr (BS) {
+    auto fold = [&](auto qc, auto livec) {
+        if constexpr (BS && decltype(qc)::value / TN < decltype(livec)::value) {
             constexpr int Q = decltype(qc)::value;
             constexpr int i = Q / TN;
             constexpr int j = (i & 1) ? (TN - 1 - Q % TN) : (Q % TN);
@@ -1024,8 +1025,13 @@ __global__ void __launch_bounds__(128 * WN, 1)
     //  Region B: fetch the A rows of stage t+4 (SPLIT) into stage t's slot
     //  (its last reads were before the barrier); read stage t+1's first
     //  fragments and its scale chunk; multiply the rest of stage t.
-    auto stage = [&](int t, auto jc) {
+    //  LIVE: the row blocks of the wave that hold rows (grouped: a tile often
+    //  ends early); the others are neither read nor multiplied.
+    auto stage = [&](int t, auto jc, auto livec) {
         constexpr int J = decltype(jc)::value;             // t % 4 (P6: t % 6, the slot)
+        constexpr int LIVE = decltype(livec)::value;
+        // item k of a sub-step: A row block 0, the B column blocks, A row blocks 1..
+        auto item_live = [](int k) constexpr { return LIVE > 0 && (k <= TN || k - TN < LIVE); };
         constexpr int JN = P6 ? (J + 1) % 6 : (J + 1) & 3;
         constexpr int SET0 = (NSUB == 1) ? (J & 1) : 0;    // register set of sub-step 0
         constexpr int SETN = (NSUB == 1) ? ((J + 1) & 1) : 0;
@@ -1065,16 +1071,18 @@ __global__ void __launch_bounds__(128 * WN, 1)
                 constexpr int Q = decltype(qc)::value;
                 static_for<(Q < NR ? R * Q / NR : R), (Q < NR ? R * (Q + 1) / NR : R)>([&](auto kc) {
                     constexpr int k = decltype(kc)::value;
-                    if constexpr (NSUB == 2)
+                    if constexpr (!item_live(NSUB == 2 ? k : EARLY + k)) {
+                    } else if constexpr (NSUB == 2)
                         read_item(kc, I1(), jc, I1(), t);
                     else
                         read_item(std::integral_constant<int, EARLY + k>(), I0(), jc,
                                   std::integral_constant<int, SET0>(), t);
                 });
                 if (mul)
-                    mfmas(I0(), std::integral_constant<int, SET0>(), qc, std::integral_constant<int, Q + 1>(), jc);
+                    mfmas(I0(), std::integral_constant<int, SET0>(), qc, std::integral_constant<int, Q + 1>(), jc,
+                          livec);
                 if constexpr (FOLD_ODD && (J & 1) && Q >= 1)
-                    fold(std::integral_constant<int, Q - 1>());
+                    fold(std::integral_constant<int, Q - 1>(), livec);
                 static_for<V * Q / NA, V * (Q + 1) / NA>([&](auto vc) {
                     constexpr int v = decltype(vc)::value;
                     if constexpr (v < NPH)
@@ -1090,7 +1098,7 @@ __global__ void __launch_bounds__(128 * WN, 1)
                     __builtin_amdgcn_sched_barrier(0);
             });
             if constexpr (FOLD_ODD && (J & 1))
-                fold(std::integral_constant<int, NA - 1>());
+                fold(std::integral_constant<int, NA - 1>(), livec);
         }
         // loads issued after stage t+1's: stages t+2 and t+3, plus the scale
         // chunk when it went out at stage t or t-1.  FP6 (round v, t = 4v + J;
@@ -1133,21 +1141,22 @@ __global__ void __launch_bounds__(128 * WN, 1)
             constexpr bool CHUNK = SCL && JN == 0;         // stage t+1 starts a round
             constexpr int R = EARLY;
             constexpr int NR = NB > 2 ? NB - 2 : 1;
-            if constexpr (CHUNK)
+            if constexpr (CHUNK && LIVE > 0)
                 load_chunk(t + 1);
             static_for<0, NB>([&](auto qc) {
                 constexpr int Q = decltype(qc)::value;
                 static_for<(Q < NR ? R * Q / NR : R), (Q < NR ? R * (Q + 1) / NR : R)>([&](auto kc) {
-                    read_item(kc, I0(), std::integral_constant<int, JN>(), std::integral_constant<int, SETN>(),
-                              t + 1);
+                    if constexpr (item_live(decltype(kc)::value))
+                        read_item(kc, I0(), std::integral_constant<int, JN>(), std::integral_constant<int, SETN>(),
+                                  t + 1);
                 });
                 if constexpr (NSUB == 2)
-                    mfmas(I1(), I1(), qc, std::integral_constant<int, Q + 1>(), jc);
+                    mfmas(I1(), I1(), qc, std::integral_constant<int, Q + 1>(), jc, livec);
                 else if (mul)
                     mfmas(I0(), std::integral_constant<int, SET0>(), std::integral_constant<int, QB + Q>(),
-                          std::integral_constant<int, QB + Q + 1>(), jc);
+                          std::integral_constant<int, QB + Q + 1>(), jc, livec);
                 if constexpr (FOLD_ODD && (J & 1) && Q >= 1)
-                    fold(std::integral_constant<int, QB + Q - 1>());
+                    fold(std::integral_constant<int, QB + Q - 1>(), livec);
                 static_for<V * Q / NB, V * (Q + 1) / NB>([&](auto vc) {
                     constexpr int v = decltype(vc)::value;
                     if constexpr (P6)
@@ -1167,10 +1176,12 @@ __global__ void __launch_bounds__(128 * WN, 1)
                     __builtin_amdgcn_sched_barrier(0);
             });
             if constexpr (FOLD_ODD && (J & 1))
-                fold(std::integral_constant<int, QB + NB - 1>());
-            read_scales(t + 1, std::integral_constant<int, JN>(), std::true_type());
+                fold(std::integral_constant<int, QB + NB - 1>(), livec);
+            if constexpr (LIVE > 0)
+                read_scales(t + 1, std::integral_constant<int, JN>(), std::true_type());
         }
-        use_next_scales();
+        if constexpr (LIVE > 0)
+            use_next_scales();
         if constexpr (FENCE)
             __builtin_amdgcn_sched_barrier(0);
         twin_sync();
@@ -1185,15 +1196,32 @@ __global__ void __launch_bounds__(128 * WN, 1)
     // Fetches run three stages (FP6: two to three lines) ahead, into stages
     // past K that are never multiplied or, in a partial last round,
     // multiplied as zeros (FP6: skipped).
+    using All = std::integral_constant<int, TM>;
     if constexpr (P6) {
         for (int t = 0; t < nst; t += 6)
-            static_for<0, 6>([&](auto jc) { stage(t + decltype(jc)::value, jc); });
+            static_for<0, 6>([&](auto jc) { stage(t + decltype(jc)::value, jc, All()); });
+    } else if constexpr (GROUPED) {
+        // The wave's rows choose the form; every form meets the same barriers.
+        // (256-row tiles: the 128x128 ones wait for memory, not the matrix
+        // cores; blockscale and e2m1 with bias would spill.)
+        constexpr bool FORMS = TM == 4 && !BS && !(PATH == PATH_MX4 && BIAS);
+        auto k_loop = [&](auto livec) {
+            for (int t = 0; t < nst; t += 4)
+                static_for<0, 4>([&](auto jc) { stage(t + decltype(jc)::value, jc, livec); });
+        };
+        const int live = rows_a - wm * TM * 32;
+        if (!FORMS || live > TM * 16)
+            k_loop(All());
+        else if (live > 0)
+            k_loop(std::integral_constant<int, FORMS ? TM / 2 : TM>());
+        else
+            k_loop(std::integral_constant<int, FORMS ? 0 : TM>());
     } else {
         for (int t = 0; t < nst; t += 4) {
-            stage(t, I0());
-            stage(t + 1, I1());
-            stage(t + 2, std::integral_constant<int, 2>());
-            stage(t + 3, std::integral_constant<int, 3>());
+            stage(t, I0(), All());
+            stage(t + 1, I1(), All());
+            stage(t + 2, std::integral_constant<int, 2>(), All());
+            stage(t + 3, std::integral_constant<int, 3>(), All());
         }
     }
     // Successor prefetch (e2m1 and 6-bit MX, blockscale FP8).  Once a round

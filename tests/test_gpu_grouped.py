@@ -129,6 +129,8 @@ def spread(total, experts, seed):
     ([1], 16, 128), ([0, 1, 0], 40, 256), ([3, 0, 17, 16, 1], 130, 384),
     ([20, 0, 0, 129, 300, 1], 200, 640),                              # 128x128 tiles
     ([513, 0, 256, 1, 700], 300, 512),                                # 256-row tiles
+    ([5000, 1, 3200], 200, 256),                                      # blockscale's
+    ([300, 64, 130, 192, 65], 264, 768),                              # waves with half their rows, and none
     ([1] * 100, 64, 1152), ([0] * 30 + [40] + [0] * 33, 256, 2048)])
 @pytest.mark.parametrize("top_k", [0, 3])
 def test_sizes(kind, counts, N, K, top_k):
@@ -234,7 +236,8 @@ def test_a_row_has_the_same_bits_wherever_it_stands(kind, counts, N):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("counts,N,K", [([1, 16, 5, 0, 40], 272, 384), ([90, 128, 0, 300, 1], 320, 640),
-                                        ([700, 0, 255, 513], 520, 1152), ([40] * 8, 64, 128)])
+                                        ([700, 0, 255, 513], 520, 1152), ([40] * 8, 64, 128),
+                                        ([300, 64, 130, 192, 65], 264, 768), ([5000, 1, 3200], 136, 256)])
 def test_same_bits_as_the_dense_gemm(kind, counts, N, K):
     """Each expert's rows are those of the GEMM of the same name on one of its
     tiles."""
