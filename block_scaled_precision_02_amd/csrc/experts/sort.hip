@@ -26,6 +26,7 @@ namespace {
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
 constexpr int ONE_WORKGROUP = 8192;    // slots that one workgroup sorts alone
 constexpr int MOST_BLOCKS = 256;
+constexpr int KEEP = 4;                // slots of a lane kept in registers
 
 // The lanes of the wave whose e equals this lane's, among the live ones.
 __device__ __forceinline__ uint64_t same_lanes(int e, bool live, int bits)
@@ -36,6 +37,17 @@ __device__ __forceinline__ uint64_t same_lanes(int e, bool live, int bits)
         m &= (e >> b) & 1 ? v : ~v;
     }
     return m;
+}
+
+// The sum over this lane and those below it.
+__device__ __forceinline__ int scan_lanes(int v, int lane)
+{
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int u = __shfl_up(v, off);
+        v += lane >= off ? u : 0;
+    }
+    return v;
 }
 
 __global__ void __launch_bounds__(THREADS) moe_count_kernel(SortArgs a)
@@ -60,11 +72,25 @@ template <bool MANY>
 __global__ void __launch_bounds__(THREADS) moe_sort_kernel(SortArgs a)
 {
     __shared__ int place[WAVES * MOE_MAX_EXPERTS];   // [WAVES][experts]: counts, then next places
-    __shared__ int wave_sum[WAVES + 1];
+    __shared__ int wave_sum[WAVES];
     __shared__ int before[MANY ? MOE_MAX_EXPERTS : 1], total[MANY ? MOE_MAX_EXPERTS : 1];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int E = a.experts;
     const int bits = 32 - __builtin_clz(max(E - 1, 1));
+    // this wave's slots, and the experts of the first of them (a wave seldom has
+    // more), loaded before anything else
+    const int first = MANY ? blockIdx.x * a.chunk : 0, last = MANY ? min(a.slots, first + a.chunk) : a.slots;
+    const int per = ((last - first + WAVES - 1) / WAVES + 63) / 64 * 64;
+    const int lo = min(first + wave * per, last), hi = min(lo + per, last);
+    int ids[KEEP];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int s = s0 + 64 * i + lane;
+            ids[i] = s < hi ? a.ids[s] : -1;
+        }
+    };
+    load(lo);
     for (int i = t; i < WAVES * E; i += THREADS)
         place[i] = 0;
     if constexpr (MANY) {
@@ -77,10 +103,16 @@ __global__ void __launch_bounds__(THREADS) moe_sort_kernel(SortArgs a)
         for (int i = t; i < parts * E; i += THREADS) {
             const int e = i % E, part = i / E;
             int b4 = 0, all = 0;
-            for (int b = part; b < a.blocks; b += parts) {
-                const int n = a.hist[b * E + e];
-                all += n;
-                b4 += b < (int)blockIdx.x ? n : 0;
+            for (int b0 = part; b0 < a.blocks; b0 += 8 * parts) {   // eight counts in flight
+                int n[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    n[u] = b0 + u * parts < a.blocks ? a.hist[(b0 + u * parts) * E + e] : 0;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    all += n[u];
+                    b4 += b0 + u * parts < (int)blockIdx.x ? n[u] : 0;
+                }
             }
             atomicAdd(&before[e], b4);
             atomicAdd(&total[e], all);
@@ -88,61 +120,53 @@ __global__ void __launch_bounds__(THREADS) moe_sort_kernel(SortArgs a)
     }
     __syncthreads();
 
-    // this wave's slots
-    const int first = MANY ? blockIdx.x * a.chunk : 0, last = MANY ? min(a.slots, first + a.chunk) : a.slots;
-    const int per = ((last - first + WAVES - 1) / WAVES + 63) / 64 * 64;
-    const int lo = min(first + wave * per, last), hi = min(lo + per, last);
     int *mine = place + wave * E;
-    for (int s0 = lo; s0 < hi; s0 += 64) {
-        const int s = s0 + lane;
-        const int e = s < hi ? a.ids[s] : -1;
-        const bool live = (unsigned)e < (unsigned)E;
-        const uint64_t m = same_lanes(e, live, bits);
-        if (live && (m & ((1ull << lane) - 1)) == 0)
-            mine[e] += __popcll(m);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next slots' lanes read it
+    for (int s0 = lo; s0 < hi; s0 += 64 * KEEP) {
+        if (s0 > lo)
+            load(s0);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            if (s0 + 64 * i >= hi)
+                break;
+            const int e = ids[i];
+            const bool live = (unsigned)e < (unsigned)E;
+            const uint64_t m = same_lanes(e, live, bits);
+            if (live && (m & ((1ull << lane) - 1)) == 0)
+                mine[e] += __popcll(m);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next slots' lanes read it
+        }
     }
     __syncthreads();
 
     // first places: over the waves of each expert, then over the experts
     // (thread t has expert t: experts <= THREADS)
-    int n = 0;
-    if (t < E) {
-        for (int w = 0; w < WAVES; ++w) {
-            const int c = place[w * E + t];
-            place[w * E + t] = n;
-            n += c;
-        }
-        if constexpr (MANY)
-            n = total[t];
-    }
-    int scan = n;
+    int count[WAVES], n = 0;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(scan, off);
-        scan += lane >= off ? v : 0;
+    for (int w = 0; w < WAVES; ++w)
+        count[w] = t < E ? place[w * E + t] : 0;
+    if constexpr (MANY) {
+        n = t < E ? total[t] : 0;
+    } else {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            n += count[w];
     }
+    const int scan = scan_lanes(n, lane);
     if (lane == 63)
         wave_sum[wave] = scan;
     __syncthreads();
-    if (t == 0) {
-        int sum = 0;
-        for (int w = 0; w < WAVES; ++w) {
-            const int v = wave_sum[w];
-            wave_sum[w] = sum;
-            sum += v;
-        }
-        wave_sum[WAVES] = sum;
-    }
-    __syncthreads();
-    const int at = wave_sum[wave] + scan - n;
-    const int live_rows = wave_sum[WAVES];
+    const int waves_scan = scan_lanes(lane < WAVES ? wave_sum[lane] : 0, lane);
+    const int live_rows = __builtin_amdgcn_readlane(waves_scan, WAVES - 1);
+    const int at = scan - n + (wave ? __builtin_amdgcn_readlane(waves_scan, wave - 1) : 0);
     if (t < E) {
         int base = at;
         if constexpr (MANY)
             base += before[t];
-        for (int w = 0; w < WAVES; ++w)
-            place[w * E + t] += base;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            place[w * E + t] = base;
+            base += count[w];
+        }
         if (!MANY || blockIdx.x == 0) {
             a.offsets[t] = at;
             if (t == 0)
@@ -151,22 +175,28 @@ __global__ void __launch_bounds__(THREADS) moe_sort_kernel(SortArgs a)
     }
     __syncthreads();
 
-    for (int s0 = lo; s0 < hi; s0 += 64) {
-        const int s = s0 + lane;
-        const int e = s < hi ? a.ids[s] : -1;
-        const bool live = (unsigned)e < (unsigned)E;
-        const uint64_t m = same_lanes(e, live, bits), lower = m & ((1ull << lane) - 1);
-        int p = -1;
-        if (live)
-            p = mine[e] + __popcll(lower);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read its place
-        if (live && lower == 0)
-            mine[e] += __popcll(m);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (s < hi)
-            a.position[s] = p;
-        if (live)
-            a.order[p] = s;
+    for (int s0 = lo; s0 < hi; s0 += 64 * KEEP) {
+        if (hi - lo > 64 * KEEP)
+            load(s0);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            if (s0 + 64 * i >= hi)
+                break;
+            const int s = s0 + 64 * i + lane, e = ids[i];
+            const bool live = (unsigned)e < (unsigned)E;
+            const uint64_t m = same_lanes(e, live, bits), lower = m & ((1ull << lane) - 1);
+            int p = -1;
+            if (live)
+                p = mine[e] + __popcll(lower);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read its place
+            if (live && lower == 0)
+                mine[e] += __popcll(m);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (s < hi)
+                a.position[s] = p;
+            if (live)
+                a.order[p] = s;
+        }
     }
     // places that no slot takes
     for (int r = max(live_rows, first) + t; r < last; r += THREADS)

@@ -19,25 +19,21 @@ namespace qgemm {
 
 namespace {
 
-// silu(g) u.  exp(-g) as a power of two: t = -g log2(e) rounded, and what the
-// rounding left out as a factor 1 + r ln 2, which keeps the result within a few
-// units in the last place for any g; past 2^126 the power alone (infinity or
-// zero: silu is -0 or g).
+// silu(g) u by the hardware's exp2 and reciprocal, each good to a unit in the
+// last place.  The exponent -g log2(e) is rounded once, an error of up to |g|
+// half units in exp(-g): far below what the encoder resolves wherever silu(g)
+// is not itself negligible.  (A correctly rounded exponential and division are 30
+// instructions an element more: the kernel waited for the vector units, 67 us
+// for 30001 rows of 2112 to MXFP8.)  exp(-g) = inf gives g * 0 = -0, as the
+// formula does.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
-    constexpr float L2E = 1.44269502162933349609375f, L2E_LO = 1.92596299112661746887e-8f, LN2 = 0.693147180559945f;
-    const float t = -g * L2E;
-    float e = __builtin_amdgcn_exp2f(t);
-    if (fabsf(t) < 126.0f) {
-        const float r = fmaf(-g, L2E, -t) - g * L2E_LO;
-        e = fmaf(e, r * LN2, e);
-    }
-    return g / (1.0f + e) * u;
+    const float e = __builtin_amdgcn_exp2f(-1.44269504088896340736f * g);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-__device__ __forceinline__ Piece load_y(const u32x4 *g, const u32x4 *u, int p)
+__device__ __forceinline__ Piece product(u32x4 a, u32x4 b)
 {
-    const u32x4 a = __builtin_nontemporal_load(&g[p]), b = __builtin_nontemporal_load(&u[p]);
     Piece y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -47,25 +43,45 @@ __device__ __forceinline__ Piece load_y(const u32x4 *g, const u32x4 *u, int p)
     return y;
 }
 
+__device__ __forceinline__ Piece load_y(const u32x4 *g, const u32x4 *u, int p)
+{
+    return product(__builtin_nontemporal_load(&g[p]), __builtin_nontemporal_load(&u[p]));
+}
+
 // Block forms: piece g of the launch is piece g % np of row g / np; np is a
-// multiple of a block's pieces, so that a block lies on adjacent lanes.
+// multiple of a block's pieces, so that a block lies on adjacent lanes.  A thread
+// takes PER pieces, 256 apart, all loaded first.
+constexpr int PER = 2;
+
 template <int OUT>
 __global__ void __launch_bounds__(256) swiglu_block_kernel(SwigluArgs a)
 {
     const int64_t rows = a.count ? min<int64_t>(max(*a.count - a.row0, (int64_t)0), a.M) : a.M;
     const unsigned np = a.I / 8;
-    const uint64_t g = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t total = (uint64_t)rows * np;
-    if (g - threadIdx.x >= total)
+    const uint64_t total = (uint64_t)rows * np, g0 = (uint64_t)blockIdx.x * (256 * PER);
+    if (g0 >= total)
         return;
-    const bool live = g < total;
-    const uint64_t row = live ? g / np : 0;
-    const int p = live ? (int)(g - row * np) : (int)(threadIdx.x & 15);
-    const u32x4 *x = (const u32x4 *)(a.X + row * a.ldx);
-    Piece y{};
-    if (live)
-        y = load_y(x, x + np, p);
-    emit<OUT>(y, 1.0f, 0.0f, p, live, a.Q + row * a.ldq, (uint8_t *)a.S + row * a.lds * (OUT == NORM_F8_BLOCK ? 4 : 1));
+    u32x4 gate[PER], up[PER];
+    int64_t row[PER];
+    int p[PER];
+    bool live[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint64_t g = g0 + 256 * i + threadIdx.x;
+        live[i] = g < total;
+        row[i] = live[i] ? (int64_t)(g / np) : 0;
+        p[i] = live[i] ? (int)(g - row[i] * np) : (int)(threadIdx.x & 15);
+        const u32x4 *x = (const u32x4 *)(a.X + row[i] * a.ldx) + p[i];
+        gate[i] = up[i] = u32x4{};
+        if (live[i]) {
+            gate[i] = __builtin_nontemporal_load(x);
+            up[i] = __builtin_nontemporal_load(x + np);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        emit<OUT>(product(gate[i], up[i]), 1.0f, 0.0f, p[i], live[i], a.Q + row[i] * a.ldq,
+                  (uint8_t *)a.S + row[i] * a.lds * (OUT == NORM_F8_BLOCK ? 4 : 1));
 }
 
 // Row forms.
@@ -144,7 +160,8 @@ template <int OUT>
 hipError_t launch_block(const SwigluArgs &a, hipStream_t s)
 {
     const uint64_t pieces = (uint64_t)a.M * (a.I / 8);
-    hipLaunchKernelGGL((swiglu_block_kernel<OUT>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((swiglu_block_kernel<OUT>), dim3((unsigned)((pieces + 256 * PER - 1) / (256 * PER))),
+                       dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -5,7 +5,7 @@ in the package: ValueError for arguments, RuntimeError for the device."""
 import torch
 
 from . import QGEMM_MX_E2M1, QGEMM_MX_E4M3, lib
-from .layer import _BF16, _enqueue, _new, _norm_codes, _rows, _vec
+from .layer import _BF16, _enqueue, _like, _new, _norm_codes, _rows, _scales, _vec
 
 _I32 = torch.int32
 _F32 = (torch.float32,)
@@ -15,10 +15,7 @@ def _out_rows(t, name, shape, device, stream):
     """(tensor, row stride) of a bf16 output, allocated where not given."""
     if t is None:
         return _new(shape, torch.bfloat16, device, stream), shape[1]
-    oshape, ld = _rows(t, name, (torch.bfloat16,))
-    if tuple(oshape) != shape or t.device != device:
-        raise ValueError(f"{name} must be bfloat16 {shape} on {device}, got {tuple(oshape)} on {t.device}")
-    return t, ld
+    return t, _like(t, name, shape, device, (torch.bfloat16,))
 
 
 def _choices(t, name):
@@ -44,13 +41,20 @@ def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, worksp
         raise ValueError(f"experts={experts}: need 1 to 1024")
     slots = tokens * top_k
     if offsets is None:
-        offsets = _new(experts + 1, _I32, device, stream)
+        offsets = _new((experts + 1,), _I32, device, stream)
+        po = offsets.data_ptr()
+    else:
+        po = _vec(offsets, "offsets", experts + 1, device, (_I32,))
     if order is None:
-        order = _new(slots, _I32, device, stream)
+        order = _new((slots,), _I32, device, stream)
+        pr = order.data_ptr()
+    else:
+        pr = _vec(order, "order", slots, device, (_I32,))
     if position is None:
         position = _new((tokens, top_k), _I32, device, stream)
-    po, pr, pp = (_vec(t, n, size, device, (_I32,)) for t, n, size in
-                  ((offsets, "offsets", experts + 1), (order, "order", slots), (position, "position", slots)))
+        pp = position.data_ptr()
+    else:
+        pp = _vec(position, "position", slots, device, (_I32,))
     pw = nbytes = 0
     if workspace is None:
         nbytes = L.qgemm_moe_sort_workspace(tokens, top_k, experts)
@@ -145,16 +149,7 @@ def _swiglu(entry, first, per_byte, part, dtype, sdtype, X, count, out, scale, s
     device = X.device
     pc = None if count is None else _vec(count, "count", 1, device, (_I32,))
     out, ldq = _norm_codes(out, M, I // per_byte, device, dtype, stream)
-    if not part:
-        scale = _new(M, sdtype, device, stream) if scale is None else scale
-        tail = (_vec(scale, "scale", M, device, (sdtype,)),)
-    else:
-        if scale is None:
-            scale = _new((M, I // part), sdtype, device, stream)
-        sshape, lds = _rows(scale, "scale", (sdtype,))
-        if tuple(sshape) != (M, I // part) or scale.device != device:
-            raise ValueError(f"scale must be {sdtype} [{M}, {I // part}] on {device}")
-        tail = (scale.data_ptr(), lds)
+    scale, tail = _scales(scale, M, I, part, sdtype, device, stream)
     _enqueue(entry, device, stream, *first, X.data_ptr(), ldx, pc, out.data_ptr(), ldq, *tail, M, I)
     return out, scale
 

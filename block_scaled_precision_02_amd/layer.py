@@ -2,6 +2,7 @@
 marshalling for the C entry points of the same names.  Errors as in the
 package: ValueError for arguments, RuntimeError for the device."""
 import ctypes
+import struct
 
 import torch
 
@@ -9,6 +10,8 @@ from . import (QGEMM_KV8_E4M3, QGEMM_KV8_I8, QGEMM_MX_E2M1, QGEMM_MX_E4M3, _chec
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _empty = torch.empty
+_current_device = torch._C._cuda_getDevice      # (a tensor is on the GPU: the runtime is up)
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 # These calls stand between the GEMMs of a decode step, where the host's time is
 # the step's: attributes are read once, and the device is changed only where it
@@ -19,10 +22,10 @@ def _enqueue(entry, device, stream, *args):
     """entry(*args, stream) on device; raises what it reports."""
     index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
+        stream = _current_stream(index)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = entry(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -177,9 +180,34 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
 
 # ------------------------------------------------------------ norms after and before a block
 
-class _Postnorm(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("Y", "R", "gamma_post", "gate", "gamma", "Rout")] + \
-        [(n, ctypes.c_int64) for n in ("ldy", "ldr", "ldo")] + [("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
+# qgemm_postnorm: Y, R, gamma_post, gate, gamma, Rout, their strides, eps, alpha
+_POSTNORM = struct.Struct("@6P3q2f")
+
+
+def _like(t, name, shape, device, dtypes=_BF16):
+    """The row stride of a tensor that has to have this shape."""
+    tshape, ld = _rows(t, name, dtypes)
+    if tshape != shape or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(tshape)} on {t.device}")
+    return ld
+
+
+def _scales(scale, M, K, part, sdtype, device, stream):
+    """(scale, the arguments that pass it on): one a row where part is 0, else
+    one for each part elements."""
+    if not part:
+        if scale is None:
+            scale = _new((M,), sdtype, device, stream)
+            return scale, (scale.data_ptr(),)
+        return scale, (_vec(scale, "scale", M, device, (sdtype,)),)
+    parts = K // part
+    if scale is None:
+        scale = _new((M, parts), sdtype, device, stream)
+        return scale, (scale.data_ptr(), parts)
+    sshape, lds = _rows(scale, "scale", (sdtype,))
+    if tuple(sshape) != (M, parts) or scale.device != device:
+        raise ValueError(f"scale must be {sdtype} [{M}, {parts}] on {device}")
+    return scale, (scale.data_ptr(), lds)
 
 
 def _postnorm(entry, first, per_byte, part, dtype, sdtype, Y, residual, gamma_post, gamma, eps, gate, alpha,
@@ -190,31 +218,20 @@ def _postnorm(entry, first, per_byte, part, dtype, sdtype, Y, residual, gamma_po
     M, K = shape
     if K % (part or 32):
         raise ValueError(f"K={K} is not a multiple of {part or 32}")
-    rshape, ldr = _rows(residual, "residual")
-    if rshape != shape or residual.device != device:
-        raise ValueError(f"residual must be {tuple(shape)} on {device}, got {tuple(rshape)} on {residual.device}")
+    ldr = _like(residual, "residual", shape, device)
     if residual_out is None:
         residual_out, ldo = _new(shape, torch.bfloat16, device, stream), K
     else:
-        oshape, ldo = _rows(residual_out, "residual_out")
-        if oshape != shape or residual_out.device != device:
-            raise ValueError(f"residual_out must be {tuple(shape)} on {device}, got {tuple(oshape)} on "
-                             f"{residual_out.device}")
+        ldo = _like(residual_out, "residual_out", shape, device)
     out, ldq = _norm_codes(out, M, K // per_byte, device, dtype, stream)
-    if not part:
-        scale = _new(M, sdtype, device, stream) if scale is None else scale
-        tail = (_vec(scale, "scale", M, device, (sdtype,)),)
-    else:
-        if scale is None:
-            scale = _new((M, K // part), sdtype, device, stream)
-        sshape, lds = _rows(scale, "scale", (sdtype,))
-        if tuple(sshape) != (M, K // part) or scale.device != device:
-            raise ValueError(f"scale must be {sdtype} [{M}, {K // part}] on {device}")
-        tail = (scale.data_ptr(), lds)
-    norm = _Postnorm(Y.data_ptr(), residual.data_ptr(), _vec(gamma_post, "gamma_post", K, device),
-                     None if gate is None else _vec(gate, "gate", K, device), _vec(gamma, "gamma", K, device),
-                     residual_out.data_ptr(), ldy, ldr, ldo, eps, alpha)
-    _enqueue(entry, device, stream, *first, ctypes.addressof(norm), out.data_ptr(), ldq, *tail, M, K)
+    scale, tail = _scales(scale, M, K, part, sdtype, device, stream)
+    try:
+        norm = _POSTNORM.pack(Y.data_ptr(), residual.data_ptr(), _vec(gamma_post, "gamma_post", K, device),
+                              0 if gate is None else _vec(gate, "gate", K, device), _vec(gamma, "gamma", K, device),
+                              residual_out.data_ptr(), ldy, ldr, ldo, eps, alpha)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"eps={eps}, alpha={alpha}: {e}") from None
+    _enqueue(entry, device, stream, *first, norm, out.data_ptr(), ldq, *tail, M, K)
     return out, scale, residual_out
 
 

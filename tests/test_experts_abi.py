@@ -7,7 +7,11 @@ import ctypes as c
 import pytest
 
 import block_scaled_precision_02_amd as q
-from block_scaled_precision_02_amd.layer import _Postnorm
+
+
+class Postnorm(c.Structure):
+    _fields_ = [(n, c.c_void_p) for n in ("Y", "R", "gamma_post", "gate", "gamma", "Rout")] + \
+        [(n, c.c_int64) for n in ("ldy", "ldr", "ldo")] + [("eps", c.c_float), ("alpha", c.c_float)]
 
 A, B, C, D, E, F = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000, 0x60000
 NULL, SHAPE, LAYOUT, FORMAT = (q.QGEMM_ERR_NULL_POINTER, q.QGEMM_ERR_BAD_SHAPE, q.QGEMM_ERR_BAD_LAYOUT,
@@ -41,7 +45,7 @@ def postnorm(name="f8_pertoken", fmt=0, Q=F, ldq=128, S=A, lds=4, M=2, K=128, no
     d = dict(Y=A, R=B, gamma_post=C, gate=D, gamma=E, Rout=B, ldy=128, ldr=128, ldo=128, eps=1e-6, alpha=1.0)
     d.update(kw)
     f = getattr(q.lib(), "qgemm_postnorm_quant_" + name)
-    s = _Postnorm(**d)
+    s = Postnorm(**d)
     head = (fmt,) if name == "mx" else ()
     tail = (lds,) if name in ("mx", "f8_block") else ()
     return f(*head, c.addressof(s) if norm == "ok" else norm, Q, ldq, S, *tail, M, K, None)

@@ -64,15 +64,21 @@ def formula(x):
     return (g / (1 + torch.exp(-g)) * u).numpy()
 
 
-# exp2 to one unit (2), the rest of its exponent (2), the sum, the quotient, the product
-Y_TOL = 7 * 2.0 ** -24
+# exp2 and the reciprocal to one unit in the last place (2^-23 each), the sum and
+# two products (2^-24 each), the exponent's rounding: half a unit of |g| log2(e),
+# times ln 2, so at most |g| 2^-24 (and as much for the constant's own rounding)
+def y_tol(x):
+    return (7 + 2 * x.double().cpu().chunk(2, 1)[0].abs().numpy()) * 2.0 ** -24
+
+
 Q_TOL = 4 * 2.0 ** -24          # the scale, its reciprocal, the quotient
 
 
 def check(kind, x, codes, scale):
     y = formula(x)
-    # far below the range of interest exp(-g) loses the correction: absolute
-    slack = np.abs(y) * Y_TOL + 2.0 ** -110
+    # below -87.3 the reciprocal of 1 + exp(-g) falls below binary32's normal range
+    # and y is 0: 87.3 exp(-87.3) is under 2^-119, times |u| below 32
+    slack = np.abs(y) * y_tol(x) + 2.0 ** -114
     check_codes(kind, y, slack, codes, scale, Q_TOL)
 
 
