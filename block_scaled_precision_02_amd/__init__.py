@@ -48,8 +48,8 @@ and those of a layer of experts (``experts.py``):
     qgemm_moe_combine(Y, position, weights=None, residual=None, out=None)
     qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None)  -> (dY, dweights)
     qgemm_i8_rowwise_grouped / qgemm_f8_pertoken_grouped / qgemm_f8_blockscale_grouped
-        (A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None)
-    qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None)
+        (A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None)
+    qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None)
     qgemm_swiglu_quant_i8_rowwise / _f8_pertoken / _f8_block (X, count=None, out=None, scale=None)  -> (Q, scale)
     qgemm_swiglu_quant_mx(fmt, X, ...)
 

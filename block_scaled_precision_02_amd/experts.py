@@ -2,6 +2,8 @@
 experts and back with their gradients, the grouped GEMMs, and SwiGLU between
 them.  Argument marshalling for the C entry points of the same names; errors as
 in the package: ValueError for arguments, RuntimeError for the device."""
+from operator import index
+
 import torch
 
 from . import QGEMM_MX_E2M1, QGEMM_MX_E4M3, lib
@@ -25,6 +27,16 @@ def _choices(t, name):
     return t.shape
 
 
+def _count(v, name, most):
+    try:
+        n = index(v)
+    except TypeError:
+        n = 0
+    if not 1 <= n <= most:
+        raise ValueError(f"{name}={v}: need a whole number, 1 to {most}")
+    return n
+
+
 # ------------------------------------------------------------ sort and exchange
 
 def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, workspace=None, stream=None):
@@ -37,8 +49,7 @@ def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, worksp
     allocated here if not given."""
     tokens, top_k = _choices(ids, "ids")
     device, L = ids.device, lib()
-    if isinstance(experts, bool) or not isinstance(experts, int) or not 1 <= experts <= 1024:
-        raise ValueError(f"experts={experts}: need 1 to 1024")
+    experts = _count(experts, "experts", 1024)
     slots = tokens * top_k
     if offsets is None:
         offsets = _new((experts + 1,), _I32, device, stream)
@@ -216,18 +227,21 @@ def _grouped(entry, first, dtypes, per_byte, sdtypes, sa_shape, sb_shape, A, B, 
     if (brow > 1 and sb[2] != 1) or (experts > 1 and sb[0] != N * ldb):
         raise ValueError("B must have unit stride along K and its experts N rows apart")
     K = row * per_byte
-    if not isinstance(top_k, int) or top_k < 1:
-        raise ValueError(f"top_k={top_k}: need at least 1")
     if not isinstance(offsets, torch.Tensor) or offsets.numel() != experts + 1:
         raise ValueError(f"offsets must hold {experts + 1} values")
     po = _vec(offsets, "offsets", experts + 1, device, (_I32,))
     if order is None:
-        rows, pr = a_rows, None
+        rows, pr, top_k = a_rows, None, 1
     else:
         if not isinstance(order, torch.Tensor) or order.dim() != 1:
             raise ValueError("order must be a 1-D tensor")
         rows = order.shape[0]
         pr = _vec(order, "order", rows, device, (_I32,))
+        if top_k is None:
+            if rows % max(a_rows, 1):
+                raise ValueError(f"an order of {rows} slots for {a_rows} tokens: top_k has to be given")
+            top_k = rows // a_rows if a_rows and rows else 1
+        top_k = _count(top_k, "top_k", 64)
     psa = _table(scale_a, "scale_a", sa_shape(a_rows, K), sdtypes, device)
     psb = _table(scale_b, "scale_b", sb_shape(experts, N, K), sdtypes, device)
     pb = None if bias is None else _table(bias, "bias", (experts, N), _BF16, device)
@@ -251,11 +265,11 @@ def _row_b(experts, N, K):
     return (experts, N)
 
 
-def qgemm_i8_rowwise_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+def qgemm_i8_rowwise_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
     """One qgemm_i8_rowwise per expert over its rows: rows offsets[e] ..
     offsets[e+1]-1 of the result are rows of A times B[e].  With an order (of
-    the sort) A holds the tokens and row r takes token order[r] // top_k; without
-    one A holds the rows.  A int8 [rows of A, K], B int8 [experts, N, K], scale_a
+    the sort) A holds the tokens and row r takes token order[r] // top_k (None: as
+    many slots a token as the order has for A's rows); without one A holds the rows.  A int8 [rows of A, K], B int8 [experts, N, K], scale_a
     fp32 [rows of A], scale_b fp32 [experts, N], bias bf16 [experts, N] -> bf16
     [rows, N]; rows past offsets[experts] are left as they are.  K a multiple of
     128."""
@@ -263,14 +277,14 @@ def qgemm_i8_rowwise_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=
                     offsets, order, top_k, bias, out, stream)
 
 
-def qgemm_f8_pertoken_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+def qgemm_f8_pertoken_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
     """One qgemm_f8_pertoken per expert over its rows; A, B e4m3 (uint8 or
     float8_e4m3fn), otherwise as qgemm_i8_rowwise_grouped."""
     return _grouped(lib().qgemm_f8_pertoken_grouped, (), _E4M3, 1, _F32, _row_a, _row_b, A, B, scale_a, scale_b,
                     offsets, order, top_k, bias, out, stream)
 
 
-def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None,
+def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None,
                                 stream=None):
     """One qgemm_f8_blockscale per expert over its rows; scale_a fp32
     [rows of A, K/128], scale_b fp32 [experts, ceil(N/128), K/128], otherwise as
@@ -280,7 +294,7 @@ def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top
                     out, stream)
 
 
-def qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=1, bias=None, out=None, stream=None):
+def qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
     """One qgemm_mx per expert over its rows; A, B e4m3 or e2m1 (two codes a
     byte, rows of K/2 bytes), scale_a ue8m0 [rows of A, K/32], scale_b ue8m0
     [experts, N, K/32], otherwise as qgemm_i8_rowwise_grouped."""

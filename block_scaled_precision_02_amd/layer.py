@@ -10,8 +10,9 @@ from . import (QGEMM_KV8_E4M3, QGEMM_KV8_I8, QGEMM_MX_E2M1, QGEMM_MX_E4M3, _chec
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _empty = torch.empty
-_current_device = torch._C._cuda_getDevice      # (a tensor is on the GPU: the runtime is up)
-_current_stream = torch._C._cuda_getCurrentRawStream
+# (called with a tensor on the GPU: the runtime is up; a torch without GPUs has neither)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # These calls stand between the GEMMs of a decode step, where the host's time is
 # the step's: attributes are read once, and the device is changed only where it

@@ -66,7 +66,7 @@ class ExpertLayer:
     def block(self, codes, scales, ids, weights):
         """The experts' share: quantised rows of the tokens -> bf16 [tokens, hidden]."""
         offsets, order, position = q.qgemm_moe_sort(ids, self.experts)
-        gu = self.gate_up(codes, scales, offsets, order=order, top_k=self.top_k)
+        gu = self.gate_up(codes, scales, offsets, order=order)
         codes, scales = q.qgemm_swiglu_quant_f8_block(gu, count=offsets[-1:])
         return q.qgemm_moe_combine(self.down(codes, scales, offsets), position, weights)
 

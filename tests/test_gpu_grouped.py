@@ -354,6 +354,16 @@ def test_empty_calls(kind):
     assert bool((out == 9).all())
 
 
+def test_top_k_from_the_order():
+    c = Case("i8", [5, 3, 4], 64, 128, 3, seed=1)
+    assert c.m == 4
+    assert torch.equal(c.call(top_k=None), c.call())
+    assert torch.equal(c.call(top_k=np.int64(3)), c.call())
+    c.a, c.sa = torch.cat([c.a, c.a[:1]]), torch.cat([c.sa, c.sa[:1]])
+    with pytest.raises(ValueError):
+        c.call(top_k=None)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("bad", [7, [1.0], "x"])
 def test_refusals(kind, bad):
