@@ -200,6 +200,9 @@ def declare(L):
     for kind in ("i8_rowwise", "f8_pertoken", "f8_blockscale", "mx"):
         f = getattr(L, f"qgemm_{kind}_grouped")
         f.restype, f.argtypes = st, ([ctypes.c_int] if kind == "mx" else []) + grouped
+    # what the compiled binding calls (csrc/binding/fast.cpp)
+    L.address = {n: ctypes.cast(getattr(L, n), _P).value for n in EXPORTS
+                 if n.startswith(("qgemm_moe_", "qgemm_swiglu_", "qgemm_postnorm_")) or n.endswith("_grouped")}
     L.qgemm_last_error.restype = ctypes.c_char_p
     L.qgemm_last_error.argtypes = []
     L.qgemm_status_string.restype = ctypes.c_char_p

@@ -55,6 +55,28 @@ def _compile(src, twin=False):
     return obj
 
 
+# The ordinary calls of the expert operators as a CPython extension (host code
+# only; it reaches the library through the addresses that the binding gives it).
+FAST_SRC = os.path.join(CSRC, "binding", "fast.cpp")
+FAST = os.path.join(HERE, "_fast.so")
+
+
+def _fast():
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    tmp = FAST + ".tmp"
+    cmd = ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"] +
+           [f"-isystem{d}" for d in include] + [FAST_SRC, "-o", tmp, "-L" + os.path.join(torch, "lib")] +
+           ["-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the binding's extension failed to build:\n" + r.stderr)
+    os.replace(tmp, FAST)
+
+
 def _link(objs, lib):
     tmp = lib + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
@@ -65,14 +87,17 @@ def _link(objs, lib):
 
 
 def build(jobs=None, twin=True):
-    """Build libqgemm.so and (twin=True) the conservative-sync twin
-    libqgemm_sync.so, every object compiled in one parallel pass."""
+    """Build libqgemm.so, the binding's extension _fast.so and (twin=True) the
+    conservative-sync twin libqgemm_sync.so, every object compiled in one
+    parallel pass."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(BUILD_SYNC, exist_ok=True)
     work = [(src, False) for src in SOURCES] + ([(src, True) for src in SOURCES] if twin else [])
     jobs = jobs or min(len(work), 2 * (os.cpu_count() or 4), 16)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        fast = ex.submit(_fast)
         objs = list(ex.map(lambda w: _compile(*w), work))
+        fast.result()
     _link(objs[:len(SOURCES)], LIB)
     if twin:
         _link(objs[len(SOURCES):], LIB_SYNC)

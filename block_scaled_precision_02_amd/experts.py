@@ -7,7 +7,8 @@ from operator import index
 import torch
 
 from . import QGEMM_MX_E2M1, QGEMM_MX_E4M3, lib
-from .layer import _BF16, _enqueue, _like, _new, _norm_codes, _rows, _scales, _vec
+from .layer import (_BF16, _F8_BLOCK, _F8_ROW, _I8_ROW, _MX, _enqueue, _fast, _like, _new, _norm_codes, _rows, _scales,
+                    _vec)
 
 _I32 = torch.int32
 _F32 = (torch.float32,)
@@ -47,8 +48,14 @@ def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, worksp
     outside [0, experts) have no row (position -1; order -1 past the last row).
     workspace: a uint8 tensor of at least qgemm_moe_sort_workspace(...) bytes,
     allocated here if not given."""
+    L = lib()
+    if _fast is not None and stream is None and offsets is None and order is None and position is None \
+            and workspace is None:
+        got = _fast.moe_sort(L.address["qgemm_moe_sort"], L.address["qgemm_moe_sort_workspace"], ids, experts)
+        if got is not None:
+            return got
     tokens, top_k = _choices(ids, "ids")
-    device, L = ids.device, lib()
+    device = ids.device
     experts = _count(experts, "experts", 1024)
     slots = tokens * top_k
     if offsets is None:
@@ -93,13 +100,18 @@ def qgemm_moe_gather(X, position, rows=None, out=None, stream=None):
     X bf16 [tokens, H], position int32 [tokens, top_k] -> bf16 [rows, H] (rows:
     tokens * top_k unless given); rows that no slot takes are left as they
     are."""
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.moe_gather(L.address["qgemm_moe_gather"], X, position, rows, out)
+        if got is not None:
+            return got
     tokens, top_k = _choices(position, "position")
     device = position.device
     H, ldx = _token_rows(X, "X", tokens, device)
     if out is not None:
         rows = _rows(out, "out", (torch.bfloat16,))[0][0] if rows is None else rows
     out, ldo = _out_rows(out, "out", (tokens * top_k if rows is None else rows, H), device, stream)
-    _enqueue(lib().qgemm_moe_gather, device, stream, X.data_ptr(), ldx, position.data_ptr(), out.data_ptr(), ldo,
+    _enqueue(L.qgemm_moe_gather, device, stream, X.data_ptr(), ldx, position.data_ptr(), out.data_ptr(), ldo,
              tokens, top_k, out.shape[0], H)
     return out
 
@@ -110,6 +122,11 @@ def qgemm_moe_combine(Y, position, weights=None, residual=None, out=None, stream
     [tokens, top_k], weights fp32 [tokens, top_k] (ones if None), residual bf16
     [tokens, H] (zeros if None; may be out) -> bf16 [tokens, H].  With neither
     it is the gradient of qgemm_moe_gather."""
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.moe_combine(L.address["qgemm_moe_combine"], Y, position, weights, residual, out)
+        if got is not None:
+            return got
     tokens, top_k = _choices(position, "position")
     device = position.device
     (rows, H), ldy = _rows(Y, "Y")
@@ -123,7 +140,7 @@ def qgemm_moe_combine(Y, position, weights=None, residual=None, out=None, stream
             raise ValueError(f"residual must be [{tokens}, {H}], got [{tokens}, {rH}]")
         pr = residual.data_ptr()
     out, ldo = _out_rows(out, "out", (tokens, H), device, stream)
-    _enqueue(lib().qgemm_moe_combine, device, stream, Y.data_ptr(), ldy, position.data_ptr(), pw, pr or None, ldr,
+    _enqueue(L.qgemm_moe_combine, device, stream, Y.data_ptr(), ldy, position.data_ptr(), pw, pr or None, ldr,
              out.data_ptr(), ldo, tokens, top_k, rows, H)
     return out
 
@@ -133,6 +150,11 @@ def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, s
     = weights[t, j] * dout[t]; dweights fp32 [tokens, top_k], the product of
     dout[t] and Y[position[t, j]]).  Rows of dY that no slot takes are left as
     they are; dY may be Y.  The residual's gradient is dout."""
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.moe_combine_grad(L.address["qgemm_moe_combine_grad"], dout, Y, position, weights, dY, dweights)
+        if got is not None:
+            return got
     tokens, top_k = _choices(position, "position")
     device = position.device
     H, ldd = _token_rows(dout, "dout", tokens, device)
@@ -143,7 +165,7 @@ def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, s
     dY, ldg = _out_rows(dY, "dY", (rows, H), device, stream)
     if dweights is None:
         dweights = _new((tokens, top_k), torch.float32, device, stream)
-    _enqueue(lib().qgemm_moe_combine_grad, device, stream, dout.data_ptr(), ldd, Y.data_ptr(), ldy,
+    _enqueue(L.qgemm_moe_combine_grad, device, stream, dout.data_ptr(), ldd, Y.data_ptr(), ldy,
              position.data_ptr(), pw, dY.data_ptr(), ldg, _vec(dweights, "dweights", tokens * top_k, device, _F32),
              tokens, top_k, rows, H)
     return dY, dweights
@@ -151,17 +173,23 @@ def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, s
 
 # ------------------------------------------------------------ SwiGLU
 
-def _swiglu(entry, first, per_byte, part, dtype, sdtype, X, count, out, scale, stream):
-    """part: elements a scale covers, 0 for the row."""
+def _swiglu(name, kind, X, count, out, scale, stream):
+    """kind: as for the norms (layer.py)."""
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.swiglu(L.address[name], *kind, X, count, out, scale)
+        if got is not None:
+            return got
+    fmt, per_byte, part, i8, ue8m0 = kind
     (M, wide), ldx = _rows(X, "X")
     I = wide // 2
     if wide % 2 or I % (part or 32):
         raise ValueError(f"X is [M, {wide}]: need two halves, each a multiple of {part or 32}")
     device = X.device
     pc = None if count is None else _vec(count, "count", 1, device, (_I32,))
-    out, ldq = _norm_codes(out, M, I // per_byte, device, dtype, stream)
-    scale, tail = _scales(scale, M, I, part, sdtype, device, stream)
-    _enqueue(entry, device, stream, *first, X.data_ptr(), ldx, pc, out.data_ptr(), ldq, *tail, M, I)
+    out, ldq = _norm_codes(out, M, I // per_byte, device, torch.int8 if i8 else torch.uint8, stream)
+    scale, tail = _scales(scale, M, I, part, torch.uint8 if ue8m0 else torch.float32, device, stream)
+    _enqueue(getattr(L, name), device, stream, *((fmt,) if fmt >= 0 else ()), X.data_ptr(), ldx, pc, out.data_ptr(), ldq, *tail, M, I)
     return out, scale
 
 
@@ -170,24 +198,21 @@ def qgemm_swiglu_quant_i8_rowwise(X, count=None, out=None, scale=None, stream=No
     fp32 [M]): the A operand and scale_a of qgemm_i8_rowwise and its grouped
     form.  count: int32 GPU tensor of one element (such as offsets[-1:] of the
     sort): rows from there on are left as they are."""
-    return _swiglu(lib().qgemm_swiglu_quant_i8_rowwise, (), 1, 0, torch.int8, torch.float32, X, count, out, scale,
-                   stream)
+    return _swiglu("qgemm_swiglu_quant_i8_rowwise", _I8_ROW, X, count, out, scale, stream)
 
 
 def qgemm_swiglu_quant_f8_pertoken(X, count=None, out=None, scale=None, stream=None):
     """silu(g) * u of X = [g | u] -> (e4m3 codes as uint8 [M, I], scale fp32
     [M]): the A operand and scale_a of qgemm_f8_pertoken and its grouped form;
     count as for the int8 form."""
-    return _swiglu(lib().qgemm_swiglu_quant_f8_pertoken, (), 1, 0, torch.uint8, torch.float32, X, count, out, scale,
-                   stream)
+    return _swiglu("qgemm_swiglu_quant_f8_pertoken", _F8_ROW, X, count, out, scale, stream)
 
 
 def qgemm_swiglu_quant_f8_block(X, count=None, out=None, scale=None, stream=None):
     """silu(g) * u of X = [g | u] -> (e4m3 codes as uint8 [M, I], scales fp32
     [M, I/128]): the A operand and scale_a of qgemm_f8_blockscale and its
     grouped form.  I a multiple of 128."""
-    return _swiglu(lib().qgemm_swiglu_quant_f8_block, (), 1, 128, torch.uint8, torch.float32, X, count, out, scale,
-                   stream)
+    return _swiglu("qgemm_swiglu_quant_f8_block", _F8_BLOCK, X, count, out, scale, stream)
 
 
 def qgemm_swiglu_quant_mx(fmt, X, count=None, out=None, scale=None, stream=None):
@@ -196,8 +221,7 @@ def qgemm_swiglu_quant_mx(fmt, X, count=None, out=None, scale=None, stream=None)
     and its grouped form."""
     if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
         raise ValueError(f"unknown MX format {fmt}")
-    return _swiglu(lib().qgemm_swiglu_quant_mx, (fmt,), 1 if fmt == QGEMM_MX_E4M3 else 2, 32, torch.uint8, torch.uint8,
-                   X, count, out, scale, stream)
+    return _swiglu("qgemm_swiglu_quant_mx", _MX[fmt], X, count, out, scale, stream)
 
 
 # ------------------------------------------------------------ grouped GEMMs
@@ -213,9 +237,24 @@ def _table(t, name, shape, dtypes, device):
     return t.data_ptr()
 
 
-def _grouped(entry, first, dtypes, per_byte, sdtypes, sa_shape, sb_shape, A, B, scale_a, scale_b, offsets, order, top_k,
-             bias, out, stream):
-    """sa_shape, sb_shape: of the scales, from (rows, K) and (experts, N, K)."""
+# name, MX format or -1, elements a byte, K elements a scale covers (0: the row),
+# rows of B that a scale covers (0 with int8)
+_G_I8 = ("qgemm_i8_rowwise_grouped", -1, 1, 0, 0)
+_G_F8 = ("qgemm_f8_pertoken_grouped", -1, 1, 0, 1)
+_G_BLOCK = ("qgemm_f8_blockscale_grouped", -1, 1, 128, 128)
+_G_MX = {QGEMM_MX_E4M3: ("qgemm_mx_grouped", QGEMM_MX_E4M3, 1, 32, 1),
+         QGEMM_MX_E2M1: ("qgemm_mx_grouped", QGEMM_MX_E2M1, 2, 32, 1)}
+
+
+def _grouped(kind, A, B, scale_a, scale_b, offsets, order, top_k, bias, out, stream):
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.grouped(L.address[kind[0]], *kind[1:], A, B, scale_a, scale_b, offsets, order, top_k, bias, out)
+        if got is not None:
+            return got
+    name, fmt, per_byte, part, b_rows = kind
+    dtypes = (torch.int8,) if b_rows == 0 else _E4M3 if per_byte == 1 else (torch.uint8,)
+    sdtypes = _UE8M0 if fmt >= 0 else _F32
     (a_rows, row), lda = _rows(A, "A", dtypes)
     device = A.device
     if not isinstance(B, torch.Tensor) or B.dtype not in dtypes or B.device != device or B.dim() != 3:
@@ -242,8 +281,8 @@ def _grouped(entry, first, dtypes, per_byte, sdtypes, sa_shape, sb_shape, A, B, 
                 raise ValueError(f"an order of {rows} slots for {a_rows} tokens: top_k has to be given")
             top_k = rows // a_rows if a_rows and rows else 1
         top_k = _count(top_k, "top_k", 64)
-    psa = _table(scale_a, "scale_a", sa_shape(a_rows, K), sdtypes, device)
-    psb = _table(scale_b, "scale_b", sb_shape(experts, N, K), sdtypes, device)
+    psa = _table(scale_a, "scale_a", (a_rows, K // part) if part else (a_rows,), sdtypes, device)
+    psb = _table(scale_b, "scale_b", (experts, -(-N // b_rows), K // part) if part else (experts, N), sdtypes, device)
     pb = None if bias is None else _table(bias, "bias", (experts, N), _BF16, device)
     if out is None:
         wide = N + (-N) % 8                   # the library's rule for row strides
@@ -252,36 +291,27 @@ def _grouped(entry, first, dtypes, per_byte, sdtypes, sa_shape, sb_shape, A, B, 
     else:
         out, ldc = _out_rows(out, "out", (rows, N), device, stream)
         ldc = ldc if rows > 1 else N + (-N) % 8
-    _enqueue(entry, device, stream, *first, A.data_ptr(), lda if a_rows > 1 else row, a_rows, B.data_ptr(), ldb, psa,
-             psb, po, pr, top_k, pb, out.data_ptr(), ldc, rows, experts, N, K)
+    _enqueue(getattr(L, name), device, stream, *((fmt,) if fmt >= 0 else ()), A.data_ptr(),
+             lda if a_rows > 1 else row, a_rows, B.data_ptr(), ldb, psa, psb, po, pr, top_k, pb, out.data_ptr(), ldc,
+             rows, experts, N, K)
     return out
-
-
-def _row_a(rows, K):
-    return (rows,)
-
-
-def _row_b(experts, N, K):
-    return (experts, N)
 
 
 def qgemm_i8_rowwise_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
     """One qgemm_i8_rowwise per expert over its rows: rows offsets[e] ..
     offsets[e+1]-1 of the result are rows of A times B[e].  With an order (of
     the sort) A holds the tokens and row r takes token order[r] // top_k (None: as
-    many slots a token as the order has for A's rows); without one A holds the rows.  A int8 [rows of A, K], B int8 [experts, N, K], scale_a
-    fp32 [rows of A], scale_b fp32 [experts, N], bias bf16 [experts, N] -> bf16
-    [rows, N]; rows past offsets[experts] are left as they are.  K a multiple of
-    128."""
-    return _grouped(lib().qgemm_i8_rowwise_grouped, (), (torch.int8,), 1, _F32, _row_a, _row_b, A, B, scale_a, scale_b,
-                    offsets, order, top_k, bias, out, stream)
+    many slots a token as the order has for A's rows); without one A holds the
+    rows.  A int8 [rows of A, K], B int8 [experts, N, K], scale_a fp32 [rows of A],
+    scale_b fp32 [experts, N], bias bf16 [experts, N] -> bf16 [rows, N]; rows past
+    offsets[experts] are left as they are.  K a multiple of 128."""
+    return _grouped(_G_I8, A, B, scale_a, scale_b, offsets, order, top_k, bias, out, stream)
 
 
 def qgemm_f8_pertoken_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
     """One qgemm_f8_pertoken per expert over its rows; A, B e4m3 (uint8 or
     float8_e4m3fn), otherwise as qgemm_i8_rowwise_grouped."""
-    return _grouped(lib().qgemm_f8_pertoken_grouped, (), _E4M3, 1, _F32, _row_a, _row_b, A, B, scale_a, scale_b,
-                    offsets, order, top_k, bias, out, stream)
+    return _grouped(_G_F8, A, B, scale_a, scale_b, offsets, order, top_k, bias, out, stream)
 
 
 def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None,
@@ -289,9 +319,7 @@ def qgemm_f8_blockscale_grouped(A, B, scale_a, scale_b, offsets, order=None, top
     """One qgemm_f8_blockscale per expert over its rows; scale_a fp32
     [rows of A, K/128], scale_b fp32 [experts, ceil(N/128), K/128], otherwise as
     qgemm_f8_pertoken_grouped."""
-    return _grouped(lib().qgemm_f8_blockscale_grouped, (), _E4M3, 1, _F32, lambda m, k: (m, k // 128),
-                    lambda e, n, k: (e, -(-n // 128), k // 128), A, B, scale_a, scale_b, offsets, order, top_k, bias,
-                    out, stream)
+    return _grouped(_G_BLOCK, A, B, scale_a, scale_b, offsets, order, top_k, bias, out, stream)
 
 
 def qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=None, bias=None, out=None, stream=None):
@@ -300,7 +328,4 @@ def qgemm_mx_grouped(fmt, A, B, scale_a, scale_b, offsets, order=None, top_k=Non
     [experts, N, K/32], otherwise as qgemm_i8_rowwise_grouped."""
     if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
         raise ValueError(f"unknown MX format {fmt}")
-    wide = fmt == QGEMM_MX_E4M3
-    return _grouped(lib().qgemm_mx_grouped, (fmt,), _E4M3 if wide else (torch.uint8,), 1 if wide else 2, _UE8M0,
-                    lambda m, k: (m, k // 32), lambda e, n, k: (e, n, k // 32), A, B, scale_a, scale_b, offsets, order,
-                    top_k, bias, out, stream)
+    return _grouped(_G_MX[fmt], A, B, scale_a, scale_b, offsets, order, top_k, bias, out, stream)

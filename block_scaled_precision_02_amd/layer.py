@@ -14,6 +14,14 @@ _empty = torch.empty
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
+# The compiled form of the expert operators' ordinary calls; without it, and for
+# every call that is not ordinary, the functions below go the full way.
+try:
+    from . import _fast
+    _fast.init(_current_device, _current_stream)
+except (ImportError, TypeError):
+    _fast = None
+
 # These calls stand between the GEMMs of a decode step, where the host's time is
 # the step's: attributes are read once, and the device is changed only where it
 # is not the current one.
@@ -181,6 +189,11 @@ def qgemm_rmsnorm_quant_mx(fmt, X, gamma, eps=1e-6, residual=None, residual_out=
 
 # ------------------------------------------------------------ norms after and before a block
 
+# kinds of quantised output: MX format or -1, codes a byte, elements a scale
+# covers (0: the row), int8 codes, ue8m0 scales
+_I8_ROW, _F8_ROW, _F8_BLOCK = (-1, 1, 0, 1, 0), (-1, 1, 0, 0, 0), (-1, 1, 128, 0, 0)
+_MX = {QGEMM_MX_E4M3: (QGEMM_MX_E4M3, 1, 32, 0, 1), QGEMM_MX_E2M1: (QGEMM_MX_E2M1, 2, 32, 0, 1)}
+
 # qgemm_postnorm: Y, R, gamma_post, gate, gamma, Rout, their strides, eps, alpha
 _POSTNORM = struct.Struct("@6P3q2f")
 
@@ -211,9 +224,16 @@ def _scales(scale, M, K, part, sdtype, device, stream):
     return scale, (scale.data_ptr(), lds)
 
 
-def _postnorm(entry, first, per_byte, part, dtype, sdtype, Y, residual, gamma_post, gamma, eps, gate, alpha,
-              residual_out, out, scale, stream):
-    """part: elements a scale covers, 0 for the row."""
+def _postnorm(name, kind, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream):
+    """kind: (MX format or -1, codes a byte, elements a scale covers or 0 for
+    the row, int8 codes, ue8m0 scales)."""
+    L = lib()
+    if _fast is not None and stream is None:
+        got = _fast.postnorm(L.address[name], *kind, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out, out,
+                             scale)
+        if got is not None:
+            return got
+    fmt, per_byte, part, i8, ue8m0 = kind
     shape, ldy = _rows(Y, "Y")
     device = Y.device
     M, K = shape
@@ -224,15 +244,15 @@ def _postnorm(entry, first, per_byte, part, dtype, sdtype, Y, residual, gamma_po
         residual_out, ldo = _new(shape, torch.bfloat16, device, stream), K
     else:
         ldo = _like(residual_out, "residual_out", shape, device)
-    out, ldq = _norm_codes(out, M, K // per_byte, device, dtype, stream)
-    scale, tail = _scales(scale, M, K, part, sdtype, device, stream)
+    out, ldq = _norm_codes(out, M, K // per_byte, device, torch.int8 if i8 else torch.uint8, stream)
+    scale, tail = _scales(scale, M, K, part, torch.uint8 if ue8m0 else torch.float32, device, stream)
     try:
         norm = _POSTNORM.pack(Y.data_ptr(), residual.data_ptr(), _vec(gamma_post, "gamma_post", K, device),
                               0 if gate is None else _vec(gate, "gate", K, device), _vec(gamma, "gamma", K, device),
                               residual_out.data_ptr(), ldy, ldr, ldo, eps, alpha)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"eps={eps}, alpha={alpha}: {e}") from None
-    _enqueue(entry, device, stream, *first, norm, out.data_ptr(), ldq, *tail, M, K)
+    _enqueue(getattr(L, name), device, stream, *((fmt,) if fmt >= 0 else ()), norm, out.data_ptr(), ldq, *tail, M, K)
     return out, scale, residual_out
 
 
@@ -243,23 +263,23 @@ def qgemm_postnorm_quant_i8_rowwise(Y, residual, gamma_post, gamma, eps=1e-6, ga
     codes [M, K], scale fp32 [M], h in bf16).  Y, residual bf16 [M, K];
     gamma_post, gamma, gate (ones if None) bf16 [K]; residual_out may be
     residual itself."""
-    return _postnorm(lib().qgemm_postnorm_quant_i8_rowwise, (), 1, 0, torch.int8, torch.float32, Y, residual,
-                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+    return _postnorm("qgemm_postnorm_quant_i8_rowwise", _I8_ROW, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out,
+                     out, scale, stream)
 
 
 def qgemm_postnorm_quant_f8_pertoken(Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0,
                                      residual_out=None, out=None, scale=None, stream=None):
     """The same -> (e4m3 codes as uint8 [M, K], scale fp32 [M], h in bf16)."""
-    return _postnorm(lib().qgemm_postnorm_quant_f8_pertoken, (), 1, 0, torch.uint8, torch.float32, Y, residual,
-                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+    return _postnorm("qgemm_postnorm_quant_f8_pertoken", _F8_ROW, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out,
+                     out, scale, stream)
 
 
 def qgemm_postnorm_quant_f8_block(Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None,
                                   out=None, scale=None, stream=None):
     """The same -> (e4m3 codes as uint8 [M, K], scales fp32 [M, K/128], h in
     bf16).  K a multiple of 128."""
-    return _postnorm(lib().qgemm_postnorm_quant_f8_block, (), 1, 128, torch.uint8, torch.float32, Y, residual,
-                     gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+    return _postnorm("qgemm_postnorm_quant_f8_block", _F8_BLOCK, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out,
+                     out, scale, stream)
 
 
 def qgemm_postnorm_quant_mx(fmt, Y, residual, gamma_post, gamma, eps=1e-6, gate=None, alpha=1.0, residual_out=None,
@@ -268,8 +288,8 @@ def qgemm_postnorm_quant_mx(fmt, Y, residual, gamma_post, gamma, eps=1e-6, gate=
     uint8 [M, K/32], h in bf16)."""
     if fmt not in (QGEMM_MX_E4M3, QGEMM_MX_E2M1):
         raise ValueError(f"unknown MX format {fmt}")
-    return _postnorm(lib().qgemm_postnorm_quant_mx, (fmt,), 1 if fmt == QGEMM_MX_E4M3 else 2, 32, torch.uint8,
-                     torch.uint8, Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out, out, scale, stream)
+    return _postnorm("qgemm_postnorm_quant_mx", _MX[fmt], Y, residual, gamma_post, gamma, eps, gate, alpha, residual_out,
+                     out, scale, stream)
 
 
 # ------------------------------------------------------------ 8-bit cache
