@@ -10,18 +10,21 @@ namespace {
 
 // The tile by what the host knows: the rows an expert has on average (how they
 // are spread is known on the device alone) and the most experts that can have
-// any.  One MI355X, us, experts chosen at random, some more often:
-//  * Above 96 rows an expert the 256-row tiles, bound by the matrix cores (64
-//    experts of 4096x4096: at 122 rows i8 288 and 337 on 128x128, at 66 rows 267
-//    and 270; e2m1 178 and 187, 161 and 152).  Blockscale, whose 256x128 tile has
-//    one wave a SIMD, from 2048 rows (8 of 4096x4096, 4096 rows: 714 and 749; 64
-//    of 4096x2048, 375 rows: 364 and 354).
-//  * Above 16 the 128x128 tile (64 of 4096x4096, 32 rows: i8 241, panel 247; e2m1
-//    139 and 148).
+// any.  One MI355X, us; "of random experts": some chosen more often than others,
+// else every expert has the rows named:
+//  * Above 96 rows an expert the 256-row tiles, bound by the matrix cores (32
+//    experts of 4096x4096, 190 rows: i8 156 and 191 on 128x256, e2m1 91 and 120;
+//    100 rows: 148 and 141, 73 and 71).  Blockscale, whose 256x128 tile has one
+//    wave a SIMD, from 448 rows (375 rows: 319 and 300, 512 rows: 369 and 387).
+//  * Above 16 the 128x256 tile, bound by its loads (64 of 7168x2048, 64 rows:
+//    blockscale 204, 128x128 224, panel 217; i8 199, 222 and 231), where its tiles
+//    fill the CUs they are spread over: it takes a CU for itself (8 of 4096x4096,
+//    128 tiles: i8 30, 128x128 23; 24, 384 tiles: 113 and 98; 16, 256 tiles: 44 and
+//    48).  Else 128x128, two a CU.
 //  * Up to 16 rows the weights' bytes are all that counts, and a chip full of
-//    loads: the panel where it has two workgroups a CU (64 tokens, 8 of 256
-//    experts of 2048x7168: blockscale 418, 128x128 451, stream 572; 16 tokens, 8 of
-//    128 of 4096x7168: e4m3 MX 363, 409 and 350).
+//    loads: the panel where it has two workgroups a CU (64 of 4096x7168, 16 rows:
+//    i8 321, 128x256 339, 128x128 348; 64 tokens, 8 of 256 random experts of
+//    2048x7168: blockscale 418, stream 572).
 //  * Fewer workgroups: the stream, whose waves each take 16 columns (3 tokens, 8
 //    of 64 of 2112x7168: e4m3 MX 67, panel 82, 128x128 87; one token, 2048x7168: i8
 //    23, 35 and 39) while an expert's rows are one tile of it mostly; else the
@@ -31,12 +34,14 @@ namespace {
 //    20, 128x128 24; 1024x7168: 19, 20 and 25).
 int pick_tile(int path, const GroupedArgs &a)
 {
-    const int64_t each = (a.rows + a.experts - 1) / a.experts;
-    if (each > (path == PATH_F8B ? 2048 : 96))
+    const int64_t each = (a.rows + a.experts - 1) / a.experts, with_rows = std::min<int64_t>(a.rows, a.experts);
+    if (each > (path == PATH_F8B ? 448 : 96))
         return path == PATH_F8B ? F8B256_TILE : DMA8_TILE;
-    if (each > 16)
-        return DMA128_TILE;
-    const int64_t panels = std::min<int64_t>(a.rows, a.experts) * ((a.N + PANEL_BN - 1) / PANEL_BN);
+    if (each > 16) {
+        const int64_t wide = with_rows * ((each + 127) / 128) * ((a.N + 255) / 256), rounds = (wide + 255) / 256;
+        return wide >= 768 || 8 * wide >= 7 * 256 * rounds ? WIDE128_TILE : DMA128_TILE;
+    }
+    const int64_t panels = with_rows * ((a.N + PANEL_BN - 1) / PANEL_BN);
     if (panels <= 64)
         return SKINNY16_TILE;
     if (panels >= 512)
@@ -44,8 +49,17 @@ int pick_tile(int path, const GroupedArgs &a)
     return each <= 4 ? STREAM16_TILE : DMA128_TILE;
 }
 
-int edge_m(int tile) { return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? 64 : tile_edge_m(tile); }
-int edge_n(int tile) { return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? PANEL_BN : tile_edge_n(tile); }
+int edge_m(int tile)
+{
+    return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? 64 : tile == WIDE128_TILE ? 128 : tile_edge_m(tile);
+}
+
+int edge_n(int tile)
+{
+    return tile == STREAM16_TILE ? 16 : tile == PANEL64_TILE ? PANEL_BN : tile == WIDE128_TILE ? 256 : tile_edge_n(tile);
+}
+
+int threads(int tile) { return tile == WIDE128_TILE ? 512 : tile_threads(tile); }
 
 // The most row tiles there can be: one partly filled for each expert with rows.
 int64_t most_tiles_m(int tile, const GroupedArgs &a)
@@ -61,7 +75,7 @@ bool grouped_fits(int path, const GroupedArgs &a)
 {
     const int tile = pick_tile(path, a);
     // fewer than 2^32 threads a launch
-    return most_tiles_m(tile, a) * tiles_n(tile, a) < ((int64_t)1 << 32) / tile_threads(tile);
+    return most_tiles_m(tile, a) * tiles_n(tile, a) < ((int64_t)1 << 32) / threads(tile);
 }
 
 hipError_t launch_grouped(int path, const GroupedArgs &a, hipStream_t s)
@@ -92,7 +106,13 @@ hipError_t launch_grouped(int path, const GroupedArgs &a, hipStream_t s)
     p.kblocks = a.K / 32;
     p.tiles_m = (int)most_tiles_m(tile, a);
     p.tiles_n = (int)tiles_n(tile, a);
-    p.group_m = is_skinny_tile(tile) ? 1 : 8;
+    // Tiles in the order of experts and columns (an expert's weights go by once,
+    // its rows stay in L2) up to 256 rows an expert, in groups of eight row tiles
+    // above; one MI355X, us, groups of one and of eight: 64 experts of 4096x4096 i8,
+    // 16 rows 195 and 217, 66 rows 259 and 273, 188 rows 347 and 358; of 2048x8192, 32
+    // rows 221 and 263 (eight experts' rows at one stride of 8 KB share memory
+    // channels); 32 of 4096x7168, 1024 rows 1005 and 975.
+    p.group_m = (a.rows + a.experts - 1) / a.experts <= 256 ? 1 : 8;
     p.c_cached = 1;
     p.offsets = a.offsets;
     p.order = a.order;

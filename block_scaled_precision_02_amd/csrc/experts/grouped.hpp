@@ -13,7 +13,9 @@ namespace qgemm {
 // Tiles of grouped products beside those of the host table (qgemm_launch.hpp):
 //  16 -> 16 rows by 16 columns, a wave over the whole of K (grouped_stream.hpp)
 //  17 -> 64 rows by 128 columns, B straight into registers (grouped_panel.hpp)
-constexpr int STREAM16_TILE = 16, PANEL64_TILE = 17;
+//  18 -> 128 rows by 256 columns, eight waves, fetched into LDS (qgemm_dma.hpp): an
+//        expert's rows are read half as often from L2 as by 128 columns
+constexpr int STREAM16_TILE = 16, PANEL64_TILE = 17, WIDE128_TILE = 18;
 
 // Per-path entry points, one translation unit each.
 hipError_t launch_grouped_i8(int tile, bool bias, const GroupedParams &p, hipStream_t s);
@@ -44,6 +46,9 @@ hipError_t launch_grouped_tile(int tile, const GroupedParams &p, hipStream_t s)
     switch (tile) {
     case PANEL64_TILE:
         hipLaunchKernelGGL((qgemm_panel_kernel<PATH, 4, BIAS, BROWS>), grid, dim3(PANEL_THREADS), 0, s, p);
+        break;
+    case WIDE128_TILE:
+        hipLaunchKernelGGL((qgemm_dma_kernel<PATH, 4, 2, 2, BIAS, BROWS, OUT_BF16, false, true>), grid, dim3(512), 0, s, p);
         break;
     case SKINNY16_TILE:
         hipLaunchKernelGGL((qgemm_skinny_kernel<PATH, 1, skinny_depth<PATH, 1>(), BIAS, BROWS, true>), grid, block, 0, s,

@@ -1202,7 +1202,7 @@ __global__ void __launch_bounds__(128 * WN, 1)
             static_for<0, 6>([&](auto jc) { stage(t + decltype(jc)::value, jc, All()); });
     } else if constexpr (GROUPED) {
         // The wave's rows choose the form; every form meets the same barriers.
-        // (256-row tiles: the 128x128 ones wait for memory, not the matrix
+        // (256-row tiles: the 128-row ones wait for memory, not the matrix
         // cores; blockscale and e2m1 with bias would spill.)
         constexpr bool FORMS = TM == 4 && !BS && !(PATH == PATH_MX4 && BIAS);
         auto k_loop = [&](auto livec) {

@@ -139,6 +139,20 @@ def test_sizes(kind, counts, N, K, top_k):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts,N,K", [
+    ([20, 0, 129, 1, 64, 65, 128, 0, 17, 33, 96, 40, 0, 2, 100, 31], 3801, 256),    # 15 columns of tiles, the last in part
+    ([0, 300] + [0] * 6 + [1] * 100 + [40, 90, 128, 257], 513, 640),
+    ([130] * 8 + [1], 4097, 1152)])
+@pytest.mark.parametrize("top_k", [0, 3])
+def test_tiles_of_256_columns(kind, counts, N, K, top_k):
+    c = Case(kind, counts, N, K, top_k, bias=top_k == 3, extra=top_k, seed=N + K)
+    out = torch.full((c.rows, N + (-N) % 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    c.call(out=out[:, :N])
+    c.check(out[:, :N])
+    assert bool((out[:, N:] == 9).all()) and bool((out[sum(counts):] == 9).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("rows,experts,N,K", [(60, 200, 272, 256), (500, 70, 136, 896), (3000, 24, 520, 384),
                                               (5000, 12, 264, 1280), (900, 1, 1024, 256), (2000, 1024, 48, 128),
                                               (300, 64, 1100, 640), (700, 60, 1161, 384)])
@@ -191,7 +205,7 @@ def test_rows_behind_the_last_and_strides(kind, each):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("each,N", [(4, 128), (80, 128), (280, 128), (4, 16384), (4, 4096)])
+@pytest.mark.parametrize("each,N", [(4, 128), (80, 128), (280, 128), (4, 16384), (4, 4096), (80, 14352)])
 def test_broken_offsets_and_orders_stay_in_range(kind, each, N):
     """Offsets outside the rows are clamped, tokens that are not there are zeros:
     nothing else is written."""

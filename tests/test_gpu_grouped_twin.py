@@ -32,6 +32,7 @@ def _gpu_only():
 @pytest.mark.parametrize("rows,experts,N,K", [
     (300, 64, 1040, 128), (300, 64, 1040, 1408), (500, 70, 1200, 4096),     # panels
     (700, 12, 400, 1664), (900, 16, 260, 384),                             # 128x128
+    (900, 16, 3700, 1664), (1500, 32, 2049, 256), (2000, 60, 1025, 2304),  # 128x256
     (3000, 12, 520, 1408), (2500, 5, 300, 2048),                           # 256x256
     (9000, 3, 264, 896)])                                                  # blockscale's 256x128
 def test_fast_build_equals_sync_twin(twin, monkeypatch, kind, rows, experts, N, K):
