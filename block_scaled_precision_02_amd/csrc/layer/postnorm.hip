@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(THREADS) postnorm_quant_kernel(PostnormArgs a)
 #pragma unroll
     for (int c = 0; c < KEEP; ++c) {
         const int p = t + THREADS * c;
-        emit<OUT>(keep[c], rstd, row_scale, p, p < np, q, srow);
+        emit<OUT, true>(keep[c], rstd, row_scale, p, p < np, q, srow);
     }
     // the rest of a long row: the loop's trip count is the workgroup's, so that
     // the lanes of a block stay together
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(THREADS) postnorm_quant_kernel(PostnormArgs a)
                 store_h(o, p, h);   // after the last read of r and y: o may be either
             times_gamma(h, g, p);
         }
-        emit<OUT>(h, rstd, row_scale, p, p < np, q, srow);
+        emit<OUT, true>(h, rstd, row_scale, p, p < np, q, srow);
     }
 }
 
