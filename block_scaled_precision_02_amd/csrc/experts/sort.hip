@@ -12,7 +12,9 @@
 // first places, and a second walk over the same slots hands them out.
 //
 // Few slots: one workgroup.  More: a first launch counts for each workgroup's
-// slots, in the second each workgroup sums the counts before its own.
+// slots, in the second each workgroup sums the counts before its own.  Bound by
+// latency, loads, ballots and scans one after the other (one MI355X: 64 x 8
+// choices of 256 experts 3.9 us, 32769 x 8 of 128 3.3 + 8.8 us, for 3 MB).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -4,7 +4,8 @@
 //   y = g / (1 + exp(-g)) * u       binary32, not rounded before the encoder
 //   code = enc(y / s)               s by the GEMM's scale rule
 //
-// Bound by memory: 4 bytes read and 1 written an output.  The block forms
+// Bound by memory: 4 bytes read and 1 written an output (one MI355X: 30001 x
+// 2112 to MXFP8 53 us, 6.0 TB/s; 512 x 2048 with row scales 3.3 us).  The block forms
 // (scales per 32 or 128 elements) need nothing of the rest of the row: a wave
 // takes any 64 consecutive pieces of 8 outputs.  The row forms keep a row in
 // the registers of a workgroup or, where there are many short rows, of a wave.
