@@ -96,7 +96,7 @@ EXPORTS = ("qgemm_i8_rowwise", "qgemm_i8_acc_i32", "qgemm_f8_pertoken", "qgemm_f
            "qgemm_swiglu_quant_f8_pertoken", "qgemm_swiglu_quant_f8_block", "qgemm_swiglu_quant_mx",
            "qgemm_i8_rowwise_grouped", "qgemm_f8_pertoken_grouped", "qgemm_f8_blockscale_grouped", "qgemm_mx_grouped",
            "qgemm_last_error", "qgemm_status_string", "qgemm_select_tile",
-           "qgemm_tile_rows", "qgemm_force_tile")
+           "qgemm_select_grouped_tile", "qgemm_tile_rows", "qgemm_force_tile")
 
 _lib = None
 _P = ctypes.c_void_p
@@ -209,6 +209,8 @@ def declare(L):
     L.qgemm_status_string.argtypes = [ctypes.c_int]
     L.qgemm_select_tile.restype = ctypes.c_int
     L.qgemm_select_tile.argtypes = [ctypes.c_int, _I64, _I64, _I64]
+    L.qgemm_select_grouped_tile.restype = ctypes.c_int
+    L.qgemm_select_grouped_tile.argtypes = [ctypes.c_int, _I64, _I64, _I64]
     L.qgemm_tile_rows.restype = ctypes.c_int
     L.qgemm_tile_rows.argtypes = [ctypes.c_int]
     L.qgemm_force_tile.restype = ctypes.c_int
@@ -238,6 +240,10 @@ def _check(status):
 
 def select_tile(path, M, N, K):
     return lib().qgemm_select_tile(path, M, N, K)
+
+
+def select_grouped_tile(path, rows, experts, N):
+    return lib().qgemm_select_grouped_tile(path, rows, experts, N)
 
 
 def tile_rows(tile):

@@ -62,6 +62,7 @@ struct GroupedArgs {
     int top_k, experts, N, K;
 };
 // path: qgemm::Path (I8, F8, MX8, MX4, F8B)
+int grouped_tile_id(int path, const GroupedArgs &a); // by rows, experts and N
 bool grouped_fits(int path, const GroupedArgs &a);   // in one launch
 hipError_t launch_grouped(int path, const GroupedArgs &a, hipStream_t s);
 

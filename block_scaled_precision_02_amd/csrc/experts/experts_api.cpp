@@ -356,4 +356,16 @@ qgemm_status qgemm_mx_grouped(qgemm_mx_fmt fmt, const void *A, int64_t lda, int6
                           order, top_k, bias, C, ldc, rows, experts, N, K, stream);
 }
 
+int qgemm_select_grouped_tile(int path, int64_t rows, int64_t experts, int64_t N)
+{
+    if (path < PATH_I8 || path > PATH_F8B || rows <= 0 || rows >= MOE_MAX_SLOTS || experts <= 0 ||
+        experts > MOE_MAX_EXPERTS || N <= 0 || N >= LD_LIMIT)
+        return -1;
+    GroupedArgs a = {};
+    a.rows = rows;
+    a.experts = (int)experts;
+    a.N = (int)N;
+    return grouped_tile_id(path, a);
+}
+
 }  // extern "C"

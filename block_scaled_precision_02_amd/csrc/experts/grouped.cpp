@@ -71,6 +71,8 @@ int64_t tiles_n(int tile, const GroupedArgs &a) { return ((int64_t)a.N + edge_n(
 
 }  // namespace
 
+int grouped_tile_id(int path, const GroupedArgs &a) { return pick_tile(path, a); }
+
 bool grouped_fits(int path, const GroupedArgs &a)
 {
     const int tile = pick_tile(path, a);

@@ -684,6 +684,15 @@ const char *qgemm_status_string(qgemm_status status);
  * M = 16). */
 int qgemm_select_tile(int path, int64_t M, int64_t N, int64_t K);
 
+/* The tile a grouped product takes for rows slots of experts experts and N
+ * columns (pure host logic; K does not count).  path as above, 0 to 4; returns 5,
+ * 7, 8 or 10 as above, or
+ *  16: 16 rows x 16 columns, a wave over the whole of K
+ *  17: 64 rows x 128 columns, B straight into registers
+ *  18: 128 rows x 256 columns, 8 waves, operands fetched straight into LDS
+ * -1 for a bad path or shape. */
+int qgemm_select_grouped_tile(int path, int64_t rows, int64_t experts, int64_t N);
+
 /* Rows of A one tile covers (for tiles 0-7 also the rows of B; tiles 8 and 9
  * cover 16 rows of B, tile 10 128), or 0 for an unknown id. */
 int qgemm_tile_rows(int tile);
