@@ -47,6 +47,7 @@ struct SwigluArgs {
     int64_t ldx, ldq, lds;
     int64_t row0;                             // the launch's first row
     int M, I;
+    unsigned row_mul, row_shift;              // the launch's: n / (I / 8) = n * row_mul >> 32 + row_shift
 };
 hipError_t launch_swiglu_quant(int out, const SwigluArgs &a, hipStream_t s);
 

@@ -91,7 +91,7 @@ qgemm_status swiglu_common(int out, const uint16_t *X, int64_t ldx, const int32_
     if (out >= NORM_F8_BLOCK && (lds < s_row || lds >= LD_LIMIT))
         return fail(QGEMM_ERR_BAD_LAYOUT, "lds=%lld: need >= %lld, below 2^31", (long long)lds, (long long)s_row);
     TRY(check_device());
-    const SwigluArgs a = {X, (uint8_t *)Q, S, count, ldx, ldq, lds, 0, (int)M, (int)I};
+    const SwigluArgs a = {X, (uint8_t *)Q, S, count, ldx, ldq, lds, 0, (int)M, (int)I, 0, 0};
     return launch([&] { return launch_swiglu_quant(out, a, (hipStream_t)stream); });
 }
 

@@ -4,8 +4,9 @@
 //   y = g / (1 + exp(-g)) * u       binary32, not rounded before the encoder
 //   code = enc(y / s)               s by the GEMM's scale rule
 //
-// Bound by memory: 4 bytes read and 1 written an output (one MI355X: 30001 x
-// 2112 to MXFP8 53 us, 6.0 TB/s; 512 x 2048 with row scales 3.3 us).  The block forms
+// Bound by memory, 4 bytes read and 1 written an output, and close behind it by
+// the vector units (one MI355X: 30001 x 2112 to MXFP8 54 us, 5.8 TB/s; 512 x 2048 with row
+// scales 3.3 us).  The block forms
 // (scales per 32 or 128 elements) need nothing of the rest of the row: a wave
 // takes any 64 consecutive pieces of 8 outputs.  The row forms keep a row in
 // the registers of a workgroup or, where there are many short rows, of a wave.
@@ -20,17 +21,25 @@ namespace qgemm {
 
 namespace {
 
-// silu(g) u by the hardware's exp2 and reciprocal, each good to a unit in the
-// last place.  The exponent -g log2(e) is rounded once, an error of up to |g|
-// half units in exp(-g): far below what the encoder resolves wherever silu(g)
-// is not itself negligible.  (A correctly rounded exponential and division are 30
-// instructions an element more: the kernel waited for the vector units, 67 us
-// for 30001 rows of 2112 to MXFP8.)  exp(-g) = inf gives g * 0 = -0, as the
-// formula does.
+// silu(g) u within a few units in the last place for every g: with a =
+// exp(-|g|) <= 1, silu is g / (1 + a) or g a / (1 + a), so that nothing
+// overflows and a small silu keeps a's relative error.  a = 2^n 2^z, n + z =
+// -|g| log2(e): g has 8 bits and HI, the logarithm's first part, 16, so that
+// their product is exact, n is what is whole in it and z, within a half, takes
+// the rest with the second part.  Past 400 a is 0 in any case.  1 + a lies in
+// [1, 2]; its reciprocal takes one Newton step on the hardware's.  (By one exp2
+// of the rounded exponent and the reciprocal as it comes, 11 instructions less an
+// element, the error is |g| + 4 units; 30001 x 2048 to e4m3 with row scales 50 us, by
+// this 56, to MXFP8 51 by either.)
 __device__ __forceinline__ float swiglu(float g, float u)
 {
-    const float e = __builtin_amdgcn_exp2f(-1.44269504088896340736f * g);
-    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+    constexpr float HI = 1.44268798828125f, LO = 7.052607543e-6f;   // log2(e)
+    const float m = __builtin_amdgcn_fmed3f(fabsf(g), 0.0f, 400.0f);   // (NaN: any; g brings it back)
+    const float t = m * -HI, n = __builtin_rintf(t);
+    const float a = __builtin_ldexpf(__builtin_amdgcn_exp2f(fmaf(m, -LO, t - n)), (int)n);
+    const float d = 1.0f + a, r0 = __builtin_amdgcn_rcpf(d);
+    const float r = fmaf(fmaf(-d, r0, 1.0f), r0, r0);
+    return g * (g < 0.0f ? a : 1.0f) * r * u;
 }
 
 __device__ __forceinline__ Piece product(u32x4 a, u32x4 b)
@@ -58,8 +67,8 @@ template <int OUT>
 __global__ void __launch_bounds__(256) swiglu_block_kernel(SwigluArgs a)
 {
     const int64_t rows = a.count ? min<int64_t>(max(*a.count - a.row0, (int64_t)0), a.M) : a.M;
-    const unsigned np = a.I / 8;
-    const uint64_t total = (uint64_t)rows * np, g0 = (uint64_t)blockIdx.x * (256 * PER);
+    // (a launch has at most 2^31 pieces)
+    const unsigned np = a.I / 8, total = (unsigned)rows * np, g0 = blockIdx.x * (256u * PER);
     if (g0 >= total)
         return;
     u32x4 gate[PER], up[PER];
@@ -68,16 +77,14 @@ __global__ void __launch_bounds__(256) swiglu_block_kernel(SwigluArgs a)
     bool live[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const uint64_t g = g0 + 256 * i + threadIdx.x;
+        const unsigned g = g0 + 256 * i + threadIdx.x;
         live[i] = g < total;
-        row[i] = live[i] ? (int64_t)(g / np) : 0;
-        p[i] = live[i] ? (int)(g - row[i] * np) : (int)(threadIdx.x & 15);
+        const unsigned h = live[i] ? g : threadIdx.x & 3, r = __umulhi(h, a.row_mul) >> a.row_shift;   // (any piece that is there)
+        row[i] = r;
+        p[i] = (int)(h - r * np);
         const u32x4 *x = (const u32x4 *)(a.X + row[i] * a.ldx) + p[i];
-        gate[i] = up[i] = u32x4{};
-        if (live[i]) {
-            gate[i] = __builtin_nontemporal_load(x);
-            up[i] = __builtin_nontemporal_load(x + np);
-        }
+        gate[i] = __builtin_nontemporal_load(x);
+        up[i] = __builtin_nontemporal_load(x + np);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -158,9 +165,14 @@ hipError_t launch_rows(const SwigluArgs &a, hipStream_t s)
 }
 
 template <int OUT>
-hipError_t launch_block(const SwigluArgs &a, hipStream_t s)
+hipError_t launch_block(SwigluArgs a, hipStream_t s)
 {
-    const uint64_t pieces = (uint64_t)a.M * (a.I / 8);
+    // n / d for n < 2^31, 2^(b-1) < d <= 2^b: m = ceil(2^(31+b) / d) has 32 bits, and
+    // n m / 2^(31+b) is above n / d by less than n / 2^31 of 1 / d
+    const unsigned np = a.I / 8, b = 32 - __builtin_clz(np - 1);   // (np >= 4)
+    a.row_mul = (unsigned)((((uint64_t)1 << (31 + b)) + np - 1) / np);
+    a.row_shift = b - 1;
+    const uint64_t pieces = (uint64_t)a.M * np;
     hipLaunchKernelGGL((swiglu_block_kernel<OUT>), dim3((unsigned)((pieces + 256 * PER - 1) / (256 * PER))),
                        dim3(256), 0, s, a);
     return hipGetLastError();

@@ -594,8 +594,8 @@ qgemm_status qgemm_moe_combine_grad(const uint16_t *dO, int64_t lddo, const uint
 /* silu(g) * u of X = [g | u] with quantised output: the A operand and scales of
  * the product that follows.  y = g / (1 + exp(-g)) * u in binary32, then the
  * quantiser's rule as for the norms above (i8_rowwise, f8_pertoken, f8_block,
- * mx); y itself is within (4 + |g|) 2^-23 of the formula, relative, and zero
- * for g below -87.
+ * mx); y itself is within four units in the last place (4 * 2^-23, relative) of
+ * the formula, or 2^-142 |u| (exp(-|g|) is a binary32 value).
  *   X      [M, 2 I] bf16, row stride ldx ELEMENTS (multiple of 8)
  *   count  NULL, or one int32 on the device: rows from there on are left as
  *          they are in Q and the scales (offsets + experts of the sort)
