@@ -5,8 +5,9 @@
 //   code = enc(y / s)               s by the GEMM's scale rule
 //
 // Bound by memory, 4 bytes read and 1 written an output, and close behind it by
-// the vector units (one MI355X: 30001 x 2112 to MXFP8 54 us, 5.8 TB/s; 512 x 2048 with row
-// scales 3.3 us).  The block forms
+// the vector units (one MI355X: 30001 x 2112 to MXFP8 53 us, 6.0 TB/s; 30001 x 2048 to
+// blockscale 57, to e4m3 with row scales 60; 512 x 2048 with row scales 3.3).  Quotients by
+// a scale are the divided ones, as after the norms: 4 us of the 60.  The block forms
 // (scales per 32 or 128 elements) need nothing of the rest of the row: a wave
 // takes any 64 consecutive pieces of 8 outputs.  The row forms keep a row in
 // the registers of a workgroup or, where there are many short rows, of a wave.
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(256) swiglu_block_kernel(SwigluArgs a)
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        emit<OUT>(product(gate[i], up[i]), 1.0f, 0.0f, p[i], live[i], a.Q + row[i] * a.ldq,
+        emit<OUT, true>(product(gate[i], up[i]), 1.0f, 0.0f, p[i], live[i], a.Q + row[i] * a.ldq,
                   (uint8_t *)a.S + row[i] * a.lds * (OUT == NORM_F8_BLOCK ? 4 : 1));
 }
 
@@ -138,10 +139,11 @@ __global__ void __launch_bounds__(256) swiglu_row_kernel(SwigluArgs a)
 #pragma unroll
     for (int c = 0; c < KEEP; ++c) {
         const int p = t + THREADS * c;
-        emit<OUT>(keep[c], 1.0f, s, p, p < np, q, nullptr);
+        if (p < np)                                     // (the row forms exchange nothing between lanes)
+            emit<OUT, true>(keep[c], 1.0f, s, p, true, q, nullptr);
     }
     for (int p = t + THREADS * KEEP; p < np; p += THREADS)
-        emit<OUT>(load_y(g, u, p), 1.0f, s, p, true, q, nullptr);
+        emit<OUT, true>(load_y(g, u, p), 1.0f, s, p, true, q, nullptr);
 }
 
 template <int OUT, int THREADS, int KEEP>

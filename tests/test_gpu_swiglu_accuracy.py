@@ -78,3 +78,25 @@ def test_every_gate(kind):
         x = torch.zeros(g.numel(), 256, dtype=torch.bfloat16, device="cuda")
         x[:, 3], x[:, 128 + 3] = gate, 0.75
         check(kind, x)
+
+
+@pytest.mark.parametrize("kind", ["i8", "f8", "block"])
+def test_quotients_are_the_divided_ones(kind):
+    """Rows of whole scales s and values s c, c half way between two codes: a
+    quotient that is a unit in the last place off takes the odd one."""
+    s = torch.arange(33, 256, 2, device="cuda").float()              # (silu is its gate itself)
+    if kind == "i8":
+        c, top = torch.arange(127, device="cuda") + 0.5, 127.0
+        want = torch.round(c)                                        # ties to even
+    else:
+        c = torch.cat([torch.arange(17, 32, 2, device="cuda") * 2.0 ** i for i in range(-6, 4)])
+        top, want = 448.0, c.to(torch.float8_e4m3fn).float()
+    I = 128
+    x = torch.zeros(s.numel(), 2 * I, device="cuda")
+    x[:, :I] = s[:, None]
+    x[:, I], x[:, I + 1:I + 1 + c.numel()] = top, c
+    assert torch.equal(x, x.bfloat16().float())
+    codes, scale = call(kind, x.bfloat16())
+    assert torch.equal(scale.view(-1), s)
+    got = (codes if kind == "i8" else codes.view(torch.float8_e4m3fn)).float()
+    assert bool((got[:, 0] == top).all()) and torch.equal(got[:, 1:1 + c.numel()], want.expand(s.numel(), -1))
