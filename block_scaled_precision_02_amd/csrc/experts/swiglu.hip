@@ -10,7 +10,7 @@
 // a scale are the divided ones, as after the norms: 4 us of the 60.  The block forms
 // (scales per 32 or 128 elements) need nothing of the rest of the row: a wave
 // takes any 64 consecutive pieces of 8 outputs.  The row forms keep a row in
-// the registers of a workgroup or, where there are many short rows, of a wave.
+// the registers of a workgroup of 256 threads, however short it is.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -94,16 +94,16 @@ __global__ void __launch_bounds__(256) swiglu_block_kernel(SwigluArgs a)
 }
 
 // Row forms.
-template <int OUT, int THREADS, int KEEP>
-__global__ void __launch_bounds__(256) swiglu_row_kernel(SwigluArgs a)
+constexpr int THREADS = 256, WAVES = THREADS / 64;
+
+template <int OUT, int KEEP>
+__global__ void __launch_bounds__(THREADS) swiglu_row_kernel(SwigluArgs a)
 {
-    constexpr int ROWS = 256 / THREADS;                 // rows a workgroup
-    constexpr int WAVES = THREADS / 64;
     const int64_t rows = a.count ? min<int64_t>(max(*a.count - a.row0, (int64_t)0), a.M) : a.M;
-    const int t = threadIdx.x % THREADS;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x;
     if (row >= rows)
-        return;                                         // (a workgroup of several rows has no barrier)
+        return;
     const int np = a.I / 8;
     const u32x4 *g = (const u32x4 *)(a.X + row * a.ldx), *u = g + np;
     uint8_t *q = a.Q + row * a.ldq;
@@ -123,16 +123,14 @@ __global__ void __launch_bounds__(256) swiglu_row_kernel(SwigluArgs a)
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         top = max_nan(top, __shfl_xor(top, off));
-    if constexpr (WAVES > 1) {
-        __shared__ float wtop[WAVES];
-        if ((t & 63) == 0)
-            wtop[t >> 6] = top;
-        __syncthreads();
-        top = wtop[0];
+    __shared__ float wtop[WAVES];
+    if ((t & 63) == 0)
+        wtop[t >> 6] = top;
+    __syncthreads();
+    top = wtop[0];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w)
-            top = max_nan(top, wtop[w]);
-    }
+    for (int w = 1; w < WAVES; ++w)
+        top = max_nan(top, wtop[w]);
     const float s = top / (OUT == NORM_I8_ROW ? 127.0f : 448.0f);
     if (t == 0)
         ((float *)a.S)[row] = s;
@@ -146,24 +144,18 @@ __global__ void __launch_bounds__(256) swiglu_row_kernel(SwigluArgs a)
         emit<OUT, true>(load_y(g, u, p), 1.0f, s, p, true, q, nullptr);
 }
 
-template <int OUT, int THREADS, int KEEP>
-hipError_t launch_row(const SwigluArgs &a, hipStream_t s)
-{
-    constexpr int ROWS = 256 / THREADS;
-    hipLaunchKernelGGL((swiglu_row_kernel<OUT, THREADS, KEEP>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)), dim3(256), 0,
-                       s, a);
-    return hipGetLastError();
-}
-
 template <int OUT>
 hipError_t launch_rows(const SwigluArgs &a, hipStream_t s)
 {
     const int np = a.I / 8;
+    const dim3 grid((unsigned)a.M), block(THREADS);
     if (np <= 256)
-        return launch_row<OUT, 256, 1>(a, s);
-    if (np <= 512)
-        return launch_row<OUT, 256, 2>(a, s);
-    return launch_row<OUT, 256, 4>(a, s);
+        hipLaunchKernelGGL((swiglu_row_kernel<OUT, 1>), grid, block, 0, s, a);
+    else if (np <= 512)
+        hipLaunchKernelGGL((swiglu_row_kernel<OUT, 2>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((swiglu_row_kernel<OUT, 4>), grid, block, 0, s, a);
+    return hipGetLastError();
 }
 
 template <int OUT>
