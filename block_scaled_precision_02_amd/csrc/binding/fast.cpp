@@ -12,9 +12,10 @@
 // arguments.  It does the whole call and returns its result, or does nothing and
 // returns None: where anything about the arguments is out of the ordinary
 // (another type, layout, device or shape than the common one, or wrong) or the
-// entry point refuses.  The Python function then goes its full way, which says
+// entry point refuses them.  The Python function then goes its full way, which says
 // what is wrong.  What is taken here is a subset of what is taken there, with the
-// same result.
+// same result.  A device or launch error is raised here: part of the call may be
+// on the stream, and it must not be made again.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -26,9 +27,15 @@
 namespace {
 
 PyObject *g_get_device, *g_get_stream;   // torch._C._cuda_getDevice, _cuda_getCurrentRawStream
+PyObject *g_check;                       // raises what a status stands for
 
 // Leaves the function: the full way decides.
 struct Decline {};
+
+// Leaves the function: the call failed with this status.
+struct Failed {
+    int status;
+};
 
 void need(bool ok)
 {
@@ -171,7 +178,8 @@ Out out_scales(PyObject *o, const Place &p, at::ScalarType dtype, int64_t rows, 
     return {{rows, 1, 1, t.data_ptr()}, t, nullptr};
 }
 
-// ran: whether the call was made, after which there is no way back.
+// ran: whether the call was made, after which there is no way back.  Refused
+// arguments (status 1 to 4) leave nothing on the stream.
 template <class F, class... A>
 void enqueue(bool &ran, void *entry, A... a)
 {
@@ -179,7 +187,9 @@ void enqueue(bool &ran, void *entry, A... a)
     Py_BEGIN_ALLOW_THREADS
     status = ((F)entry)(a...);
     Py_END_ALLOW_THREADS
-    need(status == 0);
+    need(status < 1 || status > 4);
+    if (status)
+        throw Failed{status};
     ran = true;
 }
 
@@ -203,7 +213,7 @@ PyObject *pack(std::initializer_list<PyObject *> items)
     return t;
 }
 
-// f(ran), or None where the call was not made.
+// f(ran), or None where the call was not made; raises where it failed.
 template <class F>
 PyObject *attempt(Py_ssize_t got, Py_ssize_t want, F &&f)
 {
@@ -212,6 +222,12 @@ PyObject *attempt(Py_ssize_t got, Py_ssize_t want, F &&f)
         PyObject *r = nullptr;
         try {
             r = f(ran);
+        } catch (const Failed &e) {
+            PyObject *none = PyObject_CallFunction(g_check, "i", e.status);
+            if (none)
+                PyErr_Format(PyExc_RuntimeError, "the call failed with status %d", e.status);
+            Py_XDECREF(none);
+            return nullptr;
         } catch (...) {
         }
         if (r)
@@ -494,17 +510,19 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// get_device, get_stream
+// get_device, get_stream, check
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 2 || !PyCallable_Check(a[0]) || !PyCallable_Check(a[1])) {
-        PyErr_SetString(PyExc_TypeError, "init(get_device, get_stream)");
+    if (n != 3 || !PyCallable_Check(a[0]) || !PyCallable_Check(a[1]) || !PyCallable_Check(a[2])) {
+        PyErr_SetString(PyExc_TypeError, "init(get_device, get_stream, check)");
         return nullptr;
     }
     Py_INCREF(a[0]);
     Py_INCREF(a[1]);
+    Py_INCREF(a[2]);
     Py_XSETREF(g_get_device, a[0]);
     Py_XSETREF(g_get_stream, a[1]);
+    Py_XSETREF(g_check, a[2]);
     Py_RETURN_NONE;
 }
 

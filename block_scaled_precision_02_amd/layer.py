@@ -18,7 +18,7 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # every call that is not ordinary, the functions below go the full way.
 try:
     from . import _fast
-    _fast.init(_current_device, _current_stream)
+    _fast.init(_current_device, _current_stream, _check)
 except (ImportError, TypeError):
     _fast = None
 
