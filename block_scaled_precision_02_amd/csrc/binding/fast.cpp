@@ -15,7 +15,8 @@
 // entry point refuses them.  The Python function then goes its full way, which says
 // what is wrong.  What is taken here is a subset of what is taken there, with the
 // same result.  A device or launch error is raised here: part of the call may be
-// on the stream, and it must not be made again.
+// on the stream, and it must not be made again.  The entry points are called by
+// their prototypes in the library's header.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -24,7 +25,16 @@
 #include <cstdint>
 #include <cstring>
 
+#include "../../../include/qgemm.h"
+
 namespace {
+
+// An address of what a checked tensor holds, as any pointer that a prototype names.
+struct Address {
+    void *p;
+    Address(void *p = nullptr) : p(p) {}
+    template <class T> operator T *() const { return (T *)p; }
+};
 
 PyObject *g_get_device, *g_get_stream;   // torch._C._cuda_getDevice, _cuda_getCurrentRawStream
 PyObject *g_check;                       // raises what a status stands for
@@ -89,7 +99,7 @@ struct Place {
 };
 
 // A contiguous tensor of n elements.
-void *flat(PyObject *o, const Place &p, at::ScalarType dtype, int64_t n)
+Address flat(PyObject *o, const Place &p, at::ScalarType dtype, int64_t n)
 {
     const at::Tensor &t = tensor(o);
     need(t.scalar_type() == dtype && t.device() == p.device && t.numel() == n && t.is_contiguous());
@@ -99,7 +109,7 @@ void *flat(PyObject *o, const Place &p, at::ScalarType dtype, int64_t n)
 // A matrix with unit stride along its rows.
 struct Rows {
     int64_t rows, cols, ld;
-    void *data;
+    Address data;
 };
 
 Rows rows_of(const at::Tensor &t, const Place &p)
@@ -178,20 +188,32 @@ Out out_scales(PyObject *o, const Place &p, at::ScalarType dtype, int64_t rows, 
     return {{rows, 1, 1, t.data_ptr()}, t, nullptr};
 }
 
+// The entry point at an address, by its prototype.
+template <class F, class... A>
+auto enter(void *entry, A... a)
+{
+    return ((F *)entry)(a...);
+}
+
 // ran: whether the call was made, after which there is no way back.  Refused
 // arguments (status 1 to 4) leave nothing on the stream.
 template <class F, class... A>
 void enqueue(bool &ran, void *entry, A... a)
 {
-    int status;
+    qgemm_status status;
     Py_BEGIN_ALLOW_THREADS
-    status = ((F)entry)(a...);
+    status = enter<F>(entry, a...);
     Py_END_ALLOW_THREADS
-    need(status < 1 || status > 4);
-    if (status)
+    need(status < QGEMM_ERR_NULL_POINTER || status > QGEMM_ERR_BAD_FORMAT);
+    if (status != QGEMM_OK)
         throw Failed{status};
     ran = true;
 }
+
+// A prototype as a value.
+template <class T> struct Type {
+    using F = T;
+};
 
 void *entry_of(PyObject *o)
 {
@@ -242,7 +264,7 @@ PyObject *attempt(Py_ssize_t got, Py_ssize_t want, F &&f)
     Py_RETURN_NONE;
 }
 
-using P = const void *;
+using P = Address;
 using I = int64_t;
 
 // entry, workspace's entry, ids, experts
@@ -254,15 +276,15 @@ PyObject *moe_sort(PyObject *, PyObject *const *a, Py_ssize_t n)
         need(ids.scalar_type() == at::kInt && ids.dim() == 2 && ids.is_contiguous() && PyLong_CheckExact(a[3]));
         const I tokens = ids.size(0), k = ids.size(1), experts = whole(a[3]);
         need(experts >= 1 && experts <= 1024);
-        const I bytes = ((I(*)(I, I, I))entry_of(a[1]))(tokens, k, experts);
+        const I bytes = enter<decltype(qgemm_moe_sort_workspace)>(entry_of(a[1]), tokens, k, experts);
         need(bytes >= 0);
         at::Tensor offsets = fresh({experts + 1}, at::kInt, p), order = fresh({tokens * k}, at::kInt, p),
                    position = fresh({tokens, k}, at::kInt, p), ws;
         if (bytes > 0)
             ws = fresh({bytes}, at::kByte, p);
-        enqueue<int (*)(P, I, I, I, P, P, P, P, I, P)>(ran, entry_of(a[0]), ids.data_ptr(), tokens, k, experts,
-                                                       offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                                                       bytes > 0 ? ws.data_ptr() : nullptr, bytes, p.stream);
+        enqueue<decltype(qgemm_moe_sort)>(ran, entry_of(a[0]), P(ids.data_ptr()), tokens, k, experts, P(offsets.data_ptr()),
+                                          P(order.data_ptr()), P(position.data_ptr()),
+                                          P(bytes > 0 ? ws.data_ptr() : nullptr), bytes, p.stream);
         return pack({THPVariable_Wrap(offsets), THPVariable_Wrap(order), THPVariable_Wrap(position)});
     });
 }
@@ -295,8 +317,8 @@ PyObject *moe_gather(PyObject *, PyObject *const *a, Py_ssize_t n)
             rows = rows_of(a[4], p, at::kBFloat16).rows;
         need(rows >= 0);
         const Out y = out_rows(a[4], p, at::kBFloat16, rows, x.cols);
-        enqueue<int (*)(P, I, P, P, I, I, I, I, I, P)>(ran, entry_of(a[0]), x.data, x.ld, c.data, y.r.data, y.r.ld, c.tokens,
-                                                       c.k, rows, x.cols, p.stream);
+        enqueue<decltype(qgemm_moe_gather)>(ran, entry_of(a[0]), x.data, x.ld, c.data, y.r.data, y.r.ld, c.tokens, c.k, rows,
+                                            x.cols, p.stream);
         return y.object();
     });
 }
@@ -316,9 +338,8 @@ PyObject *moe_combine(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (a[4] != Py_None)
             r = rows_of(a[4], p, at::kBFloat16, c.tokens, y.cols);
         const Out o = out_rows(a[5], p, at::kBFloat16, c.tokens, y.cols);
-        enqueue<int (*)(P, I, P, P, P, I, P, I, I, I, I, I, P)>(ran, entry_of(a[0]), y.data, y.ld, c.data, w, r.data, r.ld,
-                                                                o.r.data, o.r.ld, c.tokens, c.k, y.rows, y.cols,
-                                                                p.stream);
+        enqueue<decltype(qgemm_moe_combine)>(ran, entry_of(a[0]), y.data, y.ld, c.data, w, r.data, r.ld, o.r.data, o.r.ld,
+                                             c.tokens, c.k, y.rows, y.cols, p.stream);
         return o.object();
     });
 }
@@ -340,9 +361,8 @@ PyObject *moe_combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
             dw.r.data = flat(a[6], p, at::kFloat, c.tokens * c.k);
             dw.given = a[6];
         }
-        enqueue<int (*)(P, I, P, I, P, P, P, I, P, I, I, I, I, P)>(ran, entry_of(a[0]), d.data, d.ld, y.data, y.ld, c.data, w,
-                                                                   dy.r.data, dy.r.ld, dw.r.data, c.tokens, c.k, y.rows,
-                                                                   y.cols, p.stream);
+        enqueue<decltype(qgemm_moe_combine_grad)>(ran, entry_of(a[0]), d.data, d.ld, y.data, y.ld, c.data, w, dy.r.data,
+                                                  dy.r.ld, dw.r.data, c.tokens, c.k, y.rows, y.cols, p.stream);
         return pack({dy.object(), dw.object()});
     });
 }
@@ -376,24 +396,22 @@ PyObject *swiglu(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Out o = out_codes(a[8], p, q.i8, M, I2 / q.per_byte);
         const Out s = out_scales(a[9], p, q.scale_type(), M, I2, q.part);
         void *f = entry_of(a[0]);
+        auto rows = [&](auto type) {                     // one scale a row
+            enqueue<typename decltype(type)::F>(ran, f, x.data, x.ld, count, o.r.data, o.r.ld, s.r.data, M, I2, p.stream);
+        };
         if (q.fmt >= 0)
-            enqueue<int (*)(int, P, I, P, P, I, P, I, I, I, P)>(ran, f, q.fmt, x.data, x.ld, count, o.r.data, o.r.ld, s.r.data,
-                                                                s.r.ld, M, I2, p.stream);
+            enqueue<decltype(qgemm_swiglu_quant_mx)>(ran, f, (qgemm_mx_fmt)q.fmt, x.data, x.ld, count, o.r.data, o.r.ld,
+                                                     s.r.data, s.r.ld, M, I2, p.stream);
         else if (q.part)
-            enqueue<int (*)(P, I, P, P, I, P, I, I, I, P)>(ran, f, x.data, x.ld, count, o.r.data, o.r.ld, s.r.data, s.r.ld, M,
-                                                           I2, p.stream);
+            enqueue<decltype(qgemm_swiglu_quant_f8_block)>(ran, f, x.data, x.ld, count, o.r.data, o.r.ld, s.r.data, s.r.ld,
+                                                           M, I2, p.stream);
+        else if (q.i8)
+            rows(Type<decltype(qgemm_swiglu_quant_i8_rowwise)>());
         else
-            enqueue<int (*)(P, I, P, P, I, P, I, I, P)>(ran, f, x.data, x.ld, count, o.r.data, o.r.ld, s.r.data, M, I2,
-                                                        p.stream);
+            rows(Type<decltype(qgemm_swiglu_quant_f8_pertoken)>());
         return pack({o.object(), s.object()});
     });
 }
-
-struct Postnorm {   // qgemm_postnorm
-    P Y, R, gamma_post, gate, gamma, Rout;
-    I ldy, ldr, ldo;
-    float eps, alpha;
-};
 
 // entry, the five of Quant, Y, residual, gamma_post, gamma, eps, gate, alpha,
 // residual_out, out, scale
@@ -407,7 +425,7 @@ PyObject *postnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
         const I M = y.rows, K = y.cols;
         need(K > 0 && K % (q.part ? q.part : 32) == 0);
         const Rows r = rows_of(a[7], p, at::kBFloat16, M, K);
-        Postnorm v = {};
+        qgemm_postnorm v = {};
         v.Y = y.data;
         v.R = r.data;
         v.gamma_post = flat(a[8], p, at::kBFloat16, K);
@@ -424,13 +442,18 @@ PyObject *postnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
         v.ldr = r.ld;
         v.ldo = ro.r.ld;
         void *f = entry_of(a[0]);
+        auto rows = [&](auto type) {
+            enqueue<typename decltype(type)::F>(ran, f, &v, o.r.data, o.r.ld, s.r.data, M, K, p.stream);
+        };
         if (q.fmt >= 0)
-            enqueue<int (*)(int, P, P, I, P, I, I, I, P)>(ran, f, q.fmt, &v, o.r.data, o.r.ld, s.r.data, s.r.ld, M, K,
-                                                          p.stream);
+            enqueue<decltype(qgemm_postnorm_quant_mx)>(ran, f, (qgemm_mx_fmt)q.fmt, &v, o.r.data, o.r.ld, s.r.data, s.r.ld, M,
+                                                       K, p.stream);
         else if (q.part)
-            enqueue<int (*)(P, P, I, P, I, I, I, P)>(ran, f, &v, o.r.data, o.r.ld, s.r.data, s.r.ld, M, K, p.stream);
+            enqueue<decltype(qgemm_postnorm_quant_f8_block)>(ran, f, &v, o.r.data, o.r.ld, s.r.data, s.r.ld, M, K, p.stream);
+        else if (q.i8)
+            rows(Type<decltype(qgemm_postnorm_quant_i8_rowwise)>());
         else
-            enqueue<int (*)(P, P, I, P, I, I, P)>(ran, f, &v, o.r.data, o.r.ld, s.r.data, M, K, p.stream);
+            rows(Type<decltype(qgemm_postnorm_quant_f8_pertoken)>());
         return pack({o.object(), s.object(), ro.object()});
     });
 }
@@ -500,12 +523,18 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (rows <= 1)
             c.r.ld = N + (8 - N % 8) % 8;
         void *f = entry_of(a[0]);
+        auto call = [&](auto type, auto... format) {
+            enqueue<typename decltype(type)::F>(ran, f, format..., A.data, A.ld, A.rows, P(bt.data_ptr()), ldb, sa, sb, offsets,
+                                                order, top_k, bias, c.r.data, c.r.ld, rows, E, N, K, p.stream);
+        };
         if (fmt >= 0)
-            enqueue<int (*)(int, P, I, I, P, I, P, P, P, P, I, P, P, I, I, I, I, I, P)>(ran, f, fmt, A.data, A.ld, A.rows, bt.data_ptr(), ldb, sa, sb, offsets, order, top_k, bias, c.r.data, c.r.ld,
-                rows, E, N, K, p.stream);
+            call(Type<decltype(qgemm_mx_grouped)>(), (qgemm_mx_fmt)fmt);
+        else if (b_rows == 0)
+            call(Type<decltype(qgemm_i8_rowwise_grouped)>());
+        else if (part)
+            call(Type<decltype(qgemm_f8_blockscale_grouped)>());
         else
-            enqueue<int (*)(P, I, I, P, I, P, P, P, P, I, P, P, I, I, I, I, I, P)>(ran, f, A.data, A.ld, A.rows, bt.data_ptr(), ldb, sa, sb, offsets, order, top_k, bias, c.r.data, c.r.ld, rows,
-                E, N, K, p.stream);
+            call(Type<decltype(qgemm_f8_pertoken_grouped)>());
         return c.object();
     });
 }
