@@ -301,6 +301,14 @@ struct Choices {
     }
 };
 
+// One value for each choice: [tokens, top_k].
+Address per_choice(PyObject *o, const Place &p, const Choices &c)
+{
+    const at::Tensor &t = tensor(o);
+    need(t.dim() == 2 && t.size(0) == c.tokens && t.size(1) == c.k);
+    return flat(o, p, at::kFloat, c.tokens * c.k);
+}
+
 // entry, X, position, rows, out
 PyObject *moe_gather(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -333,7 +341,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Rows y = rows_of(a[1], p, at::kBFloat16);
         P w = nullptr;
         if (a[3] != Py_None)
-            w = flat(a[3], p, at::kFloat, c.tokens * c.k);
+            w = per_choice(a[3], p, c);
         Rows r = {0, 0, 0, nullptr};
         if (a[4] != Py_None)
             r = rows_of(a[4], p, at::kBFloat16, c.tokens, y.cols);
@@ -352,13 +360,13 @@ PyObject *moe_combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Place p(position);
         const Choices c(position);
         const Rows y = rows_of(a[2], p, at::kBFloat16), d = rows_of(a[1], p, at::kBFloat16, c.tokens, y.cols);
-        P w = flat(a[4], p, at::kFloat, c.tokens * c.k);
+        P w = per_choice(a[4], p, c);
         const Out dy = out_rows(a[5], p, at::kBFloat16, y.rows, y.cols);
         Out dw = {};
         if (a[6] == Py_None) {
             dw = out_rows(a[6], p, at::kFloat, c.tokens, c.k);
         } else {
-            dw.r.data = flat(a[6], p, at::kFloat, c.tokens * c.k);
+            dw.r.data = per_choice(a[6], p, c);
             dw.given = a[6];
         }
         enqueue<decltype(qgemm_moe_combine_grad)>(ran, entry_of(a[0]), d.data, d.ld, y.data, y.ld, c.data, w, dy.r.data,

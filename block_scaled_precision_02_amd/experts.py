@@ -28,6 +28,14 @@ def _choices(t, name):
     return t.shape
 
 
+def _array(t, name, shape, dtype, device):
+    """The address of a contiguous tensor that has to have this shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
 def _count(v, name, most):
     try:
         n = index(v)
@@ -62,17 +70,17 @@ def qgemm_moe_sort(ids, experts, offsets=None, order=None, position=None, worksp
         offsets = _new((experts + 1,), _I32, device, stream)
         po = offsets.data_ptr()
     else:
-        po = _vec(offsets, "offsets", experts + 1, device, (_I32,))
+        po = _array(offsets, "offsets", (experts + 1,), _I32, device)
     if order is None:
         order = _new((slots,), _I32, device, stream)
         pr = order.data_ptr()
     else:
-        pr = _vec(order, "order", slots, device, (_I32,))
+        pr = _array(order, "order", (slots,), _I32, device)
     if position is None:
         position = _new((tokens, top_k), _I32, device, stream)
         pp = position.data_ptr()
     else:
-        pp = _vec(position, "position", slots, device, (_I32,))
+        pp = _array(position, "position", (tokens, top_k), _I32, device)
     pw = nbytes = 0
     if workspace is None:
         nbytes = L.qgemm_moe_sort_workspace(tokens, top_k, experts)
@@ -132,7 +140,7 @@ def qgemm_moe_combine(Y, position, weights=None, residual=None, out=None, stream
     (rows, H), ldy = _rows(Y, "Y")
     if Y.device != device:
         raise ValueError(f"Y must be on {device}, found on {Y.device}")
-    pw = None if weights is None else _vec(weights, "weights", tokens * top_k, device, _F32)
+    pw = None if weights is None else _array(weights, "weights", (tokens, top_k), torch.float32, device)
     pr = ldr = 0
     if residual is not None:
         rH, ldr = _token_rows(residual, "residual", tokens, device)
@@ -161,12 +169,12 @@ def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, s
     (rows, yH), ldy = _rows(Y, "Y")
     if yH != H or Y.device != device:
         raise ValueError(f"Y must be [rows, {H}] on {device}, got {tuple(Y.shape)} on {Y.device}")
-    pw = _vec(weights, "weights", tokens * top_k, device, _F32)
+    pw = _array(weights, "weights", (tokens, top_k), torch.float32, device)
     dY, ldg = _out_rows(dY, "dY", (rows, H), device, stream)
     if dweights is None:
         dweights = _new((tokens, top_k), torch.float32, device, stream)
     _enqueue(L.qgemm_moe_combine_grad, device, stream, dout.data_ptr(), ldd, Y.data_ptr(), ldy,
-             position.data_ptr(), pw, dY.data_ptr(), ldg, _vec(dweights, "dweights", tokens * top_k, device, _F32),
+             position.data_ptr(), pw, dY.data_ptr(), ldg, _array(dweights, "dweights", (tokens, top_k), torch.float32, device),
              tokens, top_k, rows, H)
     return dY, dweights
 
