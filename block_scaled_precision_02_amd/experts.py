@@ -271,7 +271,7 @@ def _grouped(kind, A, B, scale_a, scale_b, offsets, order, top_k, bias, out, str
     sb, ldb = B.stride(), B.stride(1) if N > 1 else brow
     if brow != row:
         raise ValueError(f"A has rows of {row} bytes, B of {brow}")
-    if (brow > 1 and sb[2] != 1) or (experts > 1 and sb[0] != N * ldb):
+    if (brow > 1 and sb[2] != 1) or (experts > 1 and N > 0 and sb[0] != N * ldb):
         raise ValueError("B must have unit stride along K and its experts N rows apart")
     K = row * per_byte
     if not isinstance(offsets, torch.Tensor) or offsets.numel() != experts + 1:
