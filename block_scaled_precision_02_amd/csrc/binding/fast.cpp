@@ -323,7 +323,7 @@ PyObject *moe_gather(PyObject *, PyObject *const *a, Py_ssize_t n)
             rows = whole(a[3]);
         else if (a[4] != Py_None)
             rows = rows_of(a[4], p, at::kBFloat16).rows;
-        need(rows >= 0);
+        need(rows >= 0 && rows < (I)1 << 31);
         const Out y = out_rows(a[4], p, at::kBFloat16, rows, x.cols);
         enqueue<decltype(qgemm_moe_gather)>(ran, entry_of(a[0]), x.data, x.ld, c.data, y.r.data, y.r.ld, c.tokens, c.k, rows,
                                             x.cols, p.stream);

@@ -36,13 +36,13 @@ def _array(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
-def _count(v, name, most):
+def _count(v, name, most, least=1):
     try:
         n = index(v)
     except TypeError:
-        n = 0
-    if not 1 <= n <= most:
-        raise ValueError(f"{name}={v}: need a whole number, 1 to {most}")
+        n = least - 1
+    if not least <= n <= most:
+        raise ValueError(f"{name}={v}: need a whole number, {least} to {most}")
     return n
 
 
@@ -116,8 +116,10 @@ def qgemm_moe_gather(X, position, rows=None, out=None, stream=None):
     tokens, top_k = _choices(position, "position")
     device = position.device
     H, ldx = _token_rows(X, "X", tokens, device)
-    if out is not None:
-        rows = _rows(out, "out", (torch.bfloat16,))[0][0] if rows is None else rows
+    if rows is not None:
+        rows = _count(rows, "rows", (1 << 31) - 1, 0)
+    elif out is not None:
+        rows = _rows(out, "out", (torch.bfloat16,))[0][0]
     out, ldo = _out_rows(out, "out", (tokens * top_k if rows is None else rows, H), device, stream)
     _enqueue(L.qgemm_moe_gather, device, stream, X.data_ptr(), ldx, position.data_ptr(), out.data_ptr(), ldo,
              tokens, top_k, out.shape[0], H)

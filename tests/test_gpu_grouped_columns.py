@@ -9,6 +9,7 @@ import block_scaled_precision_02_amd as q  # noqa: E402
 from block_scaled_precision_02_amd import experts, layer  # noqa: E402
 
 from tests.test_gpu_grouped import KINDS, Case  # noqa: E402
+from tests.test_gpu_moe import data  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -34,3 +35,18 @@ def test_no_columns(way, kind, counts, top_k):
     assert tuple(out.shape) == (sum(counts), 0) and out.dtype == torch.bfloat16
     given = torch.empty(sum(counts), 0, dtype=torch.bfloat16, device="cuda")
     assert c.call(out=given) is given
+
+
+@pytest.mark.parametrize("rows", [-1, -2 ** 40, 1 << 31, 1 << 70, 2.5, "x", [3], float("nan")])
+def test_gather_rows_that_are_no_number_of_rows(way, rows):
+    position, w, x, y, r = data(7, 3, 8, 64, 1)
+    with pytest.raises(ValueError):
+        q.qgemm_moe_gather(x, position, rows=rows)
+    with pytest.raises(ValueError):
+        q.qgemm_moe_gather(x, position, rows=rows, out=y)
+
+
+def test_gather_into_no_rows(way):
+    position, w, x, y, r = data(7, 3, 8, 64, 1)
+    assert q.qgemm_moe_gather(x, position, rows=0).shape == (0, 64)
+    assert q.qgemm_moe_gather(x, position, rows=21, out=y) is y
