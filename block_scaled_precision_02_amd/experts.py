@@ -106,8 +106,8 @@ def _token_rows(t, name, tokens, device):
 def qgemm_moe_gather(X, position, rows=None, out=None, stream=None):
     """Each token's row to the rows of its choices: out[position[t, j]] = X[t].
     X bf16 [tokens, H], position int32 [tokens, top_k] -> bf16 [rows, H] (rows:
-    tokens * top_k unless given); rows that no slot takes are left as they
-    are."""
+    tokens * top_k unless given); rows that no slot takes are left as they are
+    (in a new result: any values)."""
     L = lib()
     if _fast is not None and stream is None:
         got = _fast.moe_gather(L.address["qgemm_moe_gather"], X, position, rows, out)
@@ -159,7 +159,8 @@ def qgemm_moe_combine_grad(dout, Y, position, weights, dY=None, dweights=None, s
     """The gradient of qgemm_moe_combine: (dY bf16 [rows, H], dY[position[t, j]]
     = weights[t, j] * dout[t]; dweights fp32 [tokens, top_k], the product of
     dout[t] and Y[position[t, j]]).  Rows of dY that no slot takes are left as
-    they are; dY may be Y.  The residual's gradient is dout."""
+    they are (in a new dY: any values); dY may be Y.  The residual's gradient is
+    dout."""
     L = lib()
     if _fast is not None and stream is None:
         got = _fast.moe_combine_grad(L.address["qgemm_moe_combine_grad"], dout, Y, position, weights, dY, dweights)

@@ -84,7 +84,10 @@ class _Gather(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, position):
         ctx.save_for_backward(position)
-        return q.qgemm_moe_gather(x, position)
+        # rows without a choice are zeros: what they hold meets a zero gradient in
+        # the experts' weights' gradients
+        xs = torch.zeros(position.numel(), x.shape[1], dtype=x.dtype, device=x.device)
+        return q.qgemm_moe_gather(x, position, out=xs)
 
     @staticmethod
     def backward(ctx, dxs):
@@ -105,7 +108,8 @@ class _Combine(torch.autograd.Function):
 
 
 def gather(x, position):
-    """The tokens' rows in order of experts, bf16 [tokens * top_k, hidden]."""
+    """The tokens' rows in order of experts, bf16 [tokens * top_k, hidden]; zeros
+    behind the last one."""
     return _Gather.apply(x, position)
 
 
