@@ -21,9 +21,10 @@
 //    the others at the barrier, after which stage t - 1's slot is free.
 //  * Stages past K are zeros (descriptors' range), their scale words zero.
 //
-// One MI355X: 16 tokens, 8 of 128 experts of 4096x7168, e2m1 185 us, 6.5 TB/s of
-// weights; 64 experts of 4096x7168 with 16 rows each, INT8 321 us, 5.9 TB/s.  With
-// 32 or 128 rows a panel: 2 to 4% and 5 to 15% slower.
+// One MI355X: 16 tokens, 8 of 128 experts of 4096x7168, e2m1, 64 to 77 of which
+// have rows, 175 to 213 us, 5.4 to 5.7 TB/s of weights; 64 experts of 4096x7168
+// with 16 rows each, INT8 321 us, 5.9 TB/s.  With 32 or 128 rows a panel: 2 to 4% and
+// 5 to 15% slower.
 #pragma once
 #include "../qgemm_dma.hpp"
 #include "../qgemm_skinny.hpp"

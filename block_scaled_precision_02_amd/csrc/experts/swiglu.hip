@@ -6,7 +6,7 @@
 //
 // Bound by memory, 4 bytes read and 1 written an output, and close behind it by
 // the vector units (one MI355X: 30001 x 2112 to MXFP8 53 us, 6.0 TB/s; 30001 x 2048 to
-// blockscale 57, to e4m3 with row scales 60; 512 x 2048 with row scales 3.3).  Quotients by
+// blockscale 57, to e4m3 with row scales 60; 512 x 2048 with row scales 4).  Quotients by
 // a scale are the divided ones, as after the norms: 4 us of the 60.  The block forms
 // (scales per 32 or 128 elements) need nothing of the rest of the row: a wave
 // takes any 64 consecutive pieces of 8 outputs.  The row forms keep a row in
