@@ -12,7 +12,8 @@ namespace {
 // (how many there are, fewer than that where slots belong to other ranks'
 // experts, and how they are spread, is known on the device alone: 64 experts of
 // 4096x4096, 8192 slots on 4 ranks, i8 219 us, by the live rows' tile 208; 16 of
-// 2048x7168, 128 slots on 8 ranks, 36 and 53) and the most experts that can have any.  One MI355X, us; "of random experts": some chosen more often than others,
+// 2048x7168, 128 slots on 8 ranks, 36 and 53) and the most experts that can have
+// any.  One MI355X, us; "of random experts": some chosen more often than others,
 // else every expert has the rows named:
 //  * Above 96 rows an expert the 256-row tiles, bound by the matrix cores (32
 //    experts of 4096x4096, 190 rows: i8 156 and 191 on 128x256, e2m1 91 and 120;
